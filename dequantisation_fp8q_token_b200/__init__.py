@@ -23,6 +23,9 @@ fp8 matrix products on the tensor cores (tcgen05):
     fp8q_scaled_mm_blockwise  DeepEP per-token activations x DeepSeek-V3
                               128 x 128 block-scaled weight
 
+Norm and feed-forward operators (ffn.py):
+    fp8q_rms_norm_quant, fp8q_rms_norm_bwd   residual addition, root-mean-square norm and fp8 cast
+
 Allocating helpers named after the functions on the pages:
     per_token_cast_to_fp8   (DeepEP "5 Utils")
     per_token_cast_back     (DeepEP "5 Utils", the named inverse)
@@ -165,6 +168,13 @@ def lib() -> ctypes.CDLL:
             L.fp8q_sum_rows.argtypes = [p, i32, i64, i64, p, p]
             L.fp8q_scaled_mm_blockwise.restype = st
             L.fp8q_scaled_mm_blockwise.argtypes = [p, i32, p, p, i32, p, i64, i64, i64, p, i32, p, p, p]
+            f32, sz = ctypes.c_float, ctypes.c_size_t
+            L.fp8q_rms_norm_quant.restype = st
+            L.fp8q_rms_norm_quant.argtypes = [p, i32, p, p, p, i32, i64, i64, f32, i32, i32, i32, p, p, p, p, p]
+            L.fp8q_rms_norm_bwd_workspace_bytes.restype = sz
+            L.fp8q_rms_norm_bwd_workspace_bytes.argtypes = [i64, i64]
+            L.fp8q_rms_norm_bwd.restype = st
+            L.fp8q_rms_norm_bwd.argtypes = [p, p, i32, p, i32, p, p, i64, i64, p, p, p, sz, p]
             _lib = L
     return _lib
 
@@ -1061,3 +1071,10 @@ def linear_fp8_blockwise(input: torch.Tensor, weight: torch.Tensor, weight_scale
     out = torch.empty((x.shape[0], weight.shape[0]), dtype=input.dtype, device=input.device)
     fp8q_scaled_mm_blockwise(q, s, weight, weight_scale_inv, out, bias)
     return out.reshape(*input.shape[:-1], weight.shape[0])
+
+
+# the norm and feed-forward operators (they use the helpers above)
+from . import ffn as _ffn  # noqa: E402
+from .ffn import *  # noqa: E402,F401,F403
+
+__all__ += _ffn.__all__

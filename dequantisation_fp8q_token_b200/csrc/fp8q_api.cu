@@ -494,3 +494,53 @@ fp8q_status fp8q_scaled_mm_ex(const uint8_t* a, fp8q_format fa, fp8q_layout a_la
 }
 
 }  // extern "C"
+
+extern "C" {
+
+fp8q_status fp8q_rms_norm_quant(const void* x, fp8q_dtype xt, const void* residual, void* residual_out,
+                                const void* weight, fp8q_dtype wt, int64_t m, int64_t n, float eps, int group,
+                                fp8q_format fmt, fp8q_scale_rule rule, void* y, uint8_t* q, float* scale_inv,
+                                float* rstd, fp8q_stream_t stream) {
+    if (!dtype_ok(xt) || (wt != xt && wt != FP8Q_F32)) return FP8Q_ERR_BAD_DTYPE;
+    if (!rule_ok(rule)) return FP8Q_ERR_BAD_RULE;
+    if (!fmt_ok(fmt)) return FP8Q_ERR_BAD_FORMAT;
+    if (m < 0 || n < 0 || m > 0x7FFFFFFFLL || n > 0x7FFFFFFFLL || !(eps >= 0.0f)) return FP8Q_ERR_BAD_SHAPE;
+    if (q && (group < 1 || n % group != 0)) return FP8Q_ERR_BAD_SHAPE;
+    const int64_t numel = checked_mul(m, n);
+    if (numel < 0 || checked_mul(numel, dtype_bytes(xt)) < 0) return FP8Q_ERR_BAD_SHAPE;
+    if (numel == 0) return FP8Q_OK;
+    if (!x || !weight || (!y && !q) || (q && !scale_inv) || !residual != !residual_out) return FP8Q_ERR_NULL_POINTER;
+    const size_t es = dtype_bytes(xt);
+    if (!aligned(x, es) || !aligned(residual, es) || !aligned(residual_out, es) || !aligned(y, es) ||
+        !aligned(weight, dtype_bytes(wt)) || !aligned(scale_inv, 4) || !aligned(rstd, 4))
+        return FP8Q_ERR_MISALIGNED;
+    return launch_rms_norm(x, xt, residual, residual_out, weight, wt, m, n, eps, q ? group : 1, fmt, rule, y, q,
+                           scale_inv, rstd, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t fp8q_rms_norm_bwd_workspace_bytes(int64_t m, int64_t n) {
+    if (m < 0 || n < 0 || n > 0x7FFFFFFFLL) return 0;
+    return rms_norm_bwd_workspace(m, n);
+}
+
+fp8q_status fp8q_rms_norm_bwd(const void* dy, const void* r, fp8q_dtype xt, const void* weight, fp8q_dtype wt,
+                              const float* rstd, const void* dres, int64_t m, int64_t n, void* dx, void* dweight,
+                              void* workspace, size_t workspace_bytes, fp8q_stream_t stream) {
+    if (!dtype_ok(xt) || (wt != xt && wt != FP8Q_F32)) return FP8Q_ERR_BAD_DTYPE;
+    if (m < 0 || n < 0 || m > 0x7FFFFFFFLL || n > 0x7FFFFFFFLL) return FP8Q_ERR_BAD_SHAPE;
+    const int64_t numel = checked_mul(m, n);
+    if (numel < 0 || checked_mul(numel, dtype_bytes(xt)) < 0) return FP8Q_ERR_BAD_SHAPE;
+    if (n == 0 || (m == 0 && !dweight)) return FP8Q_OK;
+    if (m > 0 && (!dy || !r || !weight || !rstd || !dx)) return FP8Q_ERR_NULL_POINTER;
+    const size_t es = dtype_bytes(xt), ws = dtype_bytes(wt);
+    if (!aligned(dy, es) || !aligned(r, es) || !aligned(dres, es) || !aligned(dx, es) || !aligned(weight, ws) ||
+        !aligned(dweight, ws) || !aligned(rstd, 4))
+        return FP8Q_ERR_MISALIGNED;
+    if (m > 0 && dweight &&
+        (!workspace || !aligned(workspace, 16) || workspace_bytes < rms_norm_bwd_workspace(m, n)))
+        return FP8Q_ERR_WORKSPACE;
+    return launch_rms_norm_bwd(dy, r, xt, weight, wt, rstd, dres, m, n, dx, dweight, static_cast<float*>(workspace),
+                               reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

@@ -96,6 +96,16 @@ fp8q_status launch_transpose(const uint8_t* src, int64_t rows, int64_t cols, uin
                              cudaStream_t s);
 fp8q_status launch_sum_rows(const void* x, int xt, int64_t rows, int64_t cols, void* out, cudaStream_t s);
 
+// root-mean-square norm (rms_norm.cu): validated arguments.  y and q: at least
+// one given; `part`: rms_norm_bwd_workspace(m, n) bytes when dw is given.
+size_t rms_norm_bwd_workspace(int64_t m, int64_t n);
+fp8q_status launch_rms_norm(const void* x, int xt, const void* res, void* res_out, const void* w, int wt, int64_t m,
+                            int64_t n, float eps, int group, int fmt, int rule, void* y, uint8_t* q, float* sinv,
+                            float* rstd, cudaStream_t s);
+fp8q_status launch_rms_norm_bwd(const void* dy, const void* r, int xt, const void* w, int wt, const float* rstd,
+                                const void* dres, int64_t m, int64_t n, void* dx, void* dw, float* part,
+                                cudaStream_t s);
+
 inline fp8q_status cuda_status(cudaError_t e) { return e == cudaSuccess ? FP8Q_OK : FP8Q_ERR_CUDA; }
 
 }  // namespace fp8q

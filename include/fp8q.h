@@ -25,6 +25,8 @@
  *   fp8q_unpack_records(_ex)    payload] records (_ex: the page's packed
  *                               4-byte-header layout as well)
  *   fp8q_*_ex                   torch's rounding of the scale expressions
+ *   fp8q_rms_norm_quant, _bwd   residual addition, root-mean-square norm and
+ *                               the cast of its result; its gradient
  *   fp8q_scaled_mm_wait_test,   tests of the products' bounded waits
  *   fp8q_scaled_mm_blockwise_wait_test
  *
@@ -523,6 +525,50 @@ fp8q_status fp8q_transpose_fp8(const uint8_t* src, int64_t rows, int64_t cols, u
  */
 fp8q_status fp8q_sum_rows(const void* x, fp8q_dtype xt, int64_t rows, int64_t cols, void* out,
                           fp8q_stream_t stream);
+
+/*
+ * Root-mean-square norm with the residual's addition and an fp8 result: what
+ * stands before a product whose activations per_token_cast_to_fp8 casts, in
+ * one pass.  For each row i:
+ *   r[i][c]  = T(x[i][c] + residual[i][c])   (r = x when residual is NULL)
+ *   rstd[i]  = 1 / sqrt(sum_c r[i][c]^2 / n + eps)
+ *   v[i][c]  = r[i][c] * rstd[i] * weight[c]                  (fp32)
+ *   residual_out[i][c] = r[i][c];  y[i][c] = T(v[i][c])
+ *   q, scale_inv: fp8q_per_token_group_quant_ex of v (not of the rounded y):
+ *     1 x group amax of |v|, clamped at 1e-4, e4m3fn or e5m2, either rule.
+ * x, residual, residual_out, y: [m][n] of type xt; weight: [n] of type wt,
+ *   which is xt or FP8Q_F32; q: [m][n] codes; scale_inv: fp32 [m][n/group];
+ *   rstd: NULL or fp32 [m] (what the backward pass takes).
+ * y or q may be NULL (not both); scale_inv goes with q; residual_out goes
+ *   with residual, and may be residual or x itself (in place).  Without q,
+ *   group is not looked at.
+ * Errors: n % group != 0, group < 1, eps negative or NaN -> FP8Q_ERR_BAD_SHAPE;
+ *   wt neither xt nor fp32 -> FP8Q_ERR_BAD_DTYPE.  m == 0 or n == 0 writes
+ *   nothing.
+ */
+fp8q_status fp8q_rms_norm_quant(const void* x, fp8q_dtype xt, const void* residual, void* residual_out,
+                                const void* weight, fp8q_dtype wt, int64_t m, int64_t n, float eps, int group,
+                                fp8q_format fmt, fp8q_scale_rule rule, void* y, uint8_t* q, float* scale_inv,
+                                float* rstd, fp8q_stream_t stream);
+
+/*
+ * Its backward pass, from the gradients of y and of r:
+ *   t = dy * weight;  xhat = r * rstd
+ *   dx[i][c]   = T(rstd[i] * (t - xhat * mean over c of (t * xhat)) + dres[i][c])
+ *                (the gradient of x, and of the residual)
+ *   dweight[c] = WT(sum over i of dy[i][c] * xhat[i][c])
+ * dy, r, dres, dx: [m][n] of type xt (r: the forward's residual_out, or x);
+ *   dres may be NULL (r is not used further).  rstd: fp32 [m], the forward's.
+ * dweight: [n] of type wt, or NULL when it is not wanted.
+ * workspace: fp8q_rms_norm_bwd_workspace_bytes(m, n) bytes (asked on the
+ *   device of the call), 16-byte aligned, when dweight is given; scratch, as
+ *   fp8q_cast_per_tensor's.  Sums are fp32 in a fixed order, without atomics.
+ * The outputs must not overlap the inputs.  m == 0 writes zeros to dweight.
+ */
+size_t fp8q_rms_norm_bwd_workspace_bytes(int64_t m, int64_t n);
+fp8q_status fp8q_rms_norm_bwd(const void* dy, const void* r, fp8q_dtype xt, const void* weight, fp8q_dtype wt,
+                              const float* rstd, const void* dres, int64_t m, int64_t n, void* dx, void* dweight,
+                              void* workspace, size_t workspace_bytes, fp8q_stream_t stream);
 
 #ifdef __cplusplus
 }

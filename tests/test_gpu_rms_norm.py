@@ -1,0 +1,269 @@
+"""fp8q_rms_norm_quant and fp8q_rms_norm_bwd on a GPU against the formulas in 64 bits.
+
+Tolerances count roundings (U = 2^-24, half a step of fp32).  A row's sum of squares has only
+positive terms; a thread adds at most max(32, n / 256) of them and ten more additions join the
+threads, so its relative error is at most C = max(32, n / 256) + 10 roundings; rstd takes half of
+it and four more (mean, eps, root, reciprocal), and v two products more: REL = C / 2 + 6.  The
+backward pass's mean is such a sum of terms of either sign, so its error scales with the sum of
+their magnitudes; dw adds at most m terms and 64 more partial sums."""
+import pytest
+import torch
+
+import plain64 as P
+from gpu_util import Guarded
+
+pytestmark = pytest.mark.gpu
+
+BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+EPS = 1e-6
+
+
+def rel(n):
+    return ((max(32, n / 256) + 10) / 2 + 6) * P.U
+
+
+def make(m, n, dt, res, w32=False, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed + m * 31 + n)
+    x = (torch.randn(m, n, generator=g, device="cuda") * torch.exp(torch.randn(m, 1, generator=g, device="cuda"))).to(dt)
+    r = torch.randn(m, n, generator=g, device="cuda").to(dt) if res else None
+    w = (1 + 0.3 * torch.randn(n, generator=g, device="cuda")).to(F32 if w32 else dt)
+    return x, r, w
+
+
+def shifted(t, offset):
+    """The same values `offset` elements past an aligned address."""
+    buf = torch.zeros(t.numel() + offset, dtype=t.dtype, device=t.device)
+    buf[offset:].copy_(t.reshape(-1))
+    return buf[offset:].view(t.shape)
+
+
+def check_forward(fp8q, x, res, w, group=128, fmt=0, rule="ieee", eps=EPS, with_y=True, q_offset=0):
+    m, n = x.shape
+    q = Guarded(m * n, torch.uint8, offset=q_offset)
+    s = Guarded(m * (n // group), F32)
+    y = Guarded(m * n, x.dtype) if with_y else None
+    r = Guarded(m * n, x.dtype) if res is not None else None
+    rstd = Guarded(m, F32)
+    fp8q.fp8q_rms_norm_quant(x, w, y=y.t if with_y else None, q=q.t, scale_inv=s.t, residual=res,
+                             residual_out=r.t.view(m, n) if r else None, rstd=rstd.t, eps=eps, group=group, fmt=fmt,
+                             rule=rule)
+    for g in (q, s, y, r, rstd):
+        if g is not None:
+            g.check()
+    r64, rstd64, v = P.norm(x, w, res, eps)
+    e = rel(n)
+    assert ((rstd.t.double() - rstd64.view(-1)).abs() <= e * rstd64.view(-1)).all()
+    if r is not None:
+        assert torch.equal(r.t.view(m, n).double(), r64)
+    if with_y:
+        tol = v.abs() * (e + P.half_step(x.dtype)) + P.tiny(x.dtype)
+        assert ((y.t.view(m, n).double() - v).abs() <= tol).all()
+    P.check_groups(q.t, s.t, v, group, fmt, e)
+
+
+@pytest.mark.parametrize("dt", [BF16, F16, F32])
+@pytest.mark.parametrize("res", [False, True])
+@pytest.mark.parametrize("m,n,group", [(1, 128, 128), (1, 7168, 128), (3, 256, 64), (37, 1024, 128), (5, 1000, 8),
+                                       (4, 1000, 125), (130, 384, 32), (2, 18432, 128), (3, 32768, 256),
+                                       (2, 33024, 128), (9, 7, 7), (300, 16, 16), (2, 2048, 512), (2, 4096, 1024)])
+def test_forward(fp8q, dt, res, m, n, group):
+    x, r, w = make(m, n, dt, res)
+    check_forward(fp8q, x, r, w, group)
+
+
+@pytest.mark.parametrize("dt", [BF16, F16])
+@pytest.mark.parametrize("n,group", [(2048, 128), (1000, 100), (24576, 64)])
+def test_forward_fp32_weight_e5m2_and_no_y(fp8q, dt, n, group):
+    x, r, w = make(21, n, dt, True, w32=True)
+    check_forward(fp8q, x, r, w, group, fmt=1, rule="torch", eps=1e-5, with_y=False)
+
+
+@pytest.mark.parametrize("dt,offset", [(BF16, 1), (BF16, 8), (F16, 3), (F32, 1), (F32, 4)])
+def test_forward_unaligned(fp8q, dt, offset):
+    x, r, w = make(17, 1024, dt, True)
+    check_forward(fp8q, shifted(x, offset), shifted(r, offset), shifted(w, 1 if offset < 4 else offset), q_offset=1)
+    check_forward(fp8q, shifted(x, offset), r, w)
+
+
+def test_the_cast_is_the_per_token_cast_of_the_fp32_norm(fp8q):
+    """With fp32 rows y is the norm itself, so codes and scales equal fp8q_per_token_group_quant's
+    of y, bit for bit, under both rules and formats."""
+    x, r, w = make(67, 2048, F32, True)
+    for fmt, rule in ((0, "ieee"), (0, "torch"), (1, "ieee"), (1, "torch")):
+        y = torch.empty_like(x)
+        q, s, ro = torch.empty(67, 2048, dtype=torch.uint8, device="cuda"), torch.empty(67, 16, device="cuda"), torch.empty_like(x)
+        fp8q.fp8q_rms_norm_quant(x, w, y=y, q=q, scale_inv=s, residual=r, residual_out=ro, fmt=fmt, rule=rule)
+        q2, s2 = torch.empty_like(q), torch.empty_like(s)
+        fp8q.fp8q_per_token_group_quant_ex(y, q2, s2, 128, fmt, rule)
+        assert torch.equal(q, q2) and torch.equal(s, s2)
+
+
+@pytest.mark.parametrize("n", [1024, 1001])
+def test_zero_rows_nan_and_inf_stay_in_their_rows(fp8q, n):
+    x, _, w = make(5, n, BF16, False)
+    x[1] = 0
+    x[2, 3] = float("nan")
+    x[3, 5] = float("inf")
+    group = 128 if n % 128 == 0 else n
+    q, s = fp8q.rms_norm_cast_to_fp8(x, w, group=group)
+    y = fp8q.rms_norm(x, w)
+    assert (q[1].float() == 0).all() and torch.allclose(s[1], torch.full_like(s[1], 1e-4 / 448))
+    assert q[2].float().isnan().all() and s[2].isnan().all() and y[2].isnan().all()
+    # an infinite row: rstd is 0, so its finite elements are 0 and the infinite one NaN
+    assert y[3, 5].isnan() and (y[3, :5] == 0).all() and (y[3, 6:] == 0).all()
+    good = torch.tensor([0, 4], device="cuda")
+    v = P.norm(x[good], w, None, EPS)[2]
+    P.check_groups(q[good].contiguous().view(torch.uint8), s[good].contiguous(), v, group, 0, rel(n))
+
+
+@pytest.mark.parametrize("n", [1024, 1000, 40000])
+def test_the_sum_may_be_written_in_place(fp8q, n):
+    for over in ("residual", "x"):
+        x, r, w = make(11, n, BF16, True)
+        want_r, _, v = P.norm(x, w, r, EPS)
+        q, s = torch.empty(11, n, dtype=torch.uint8, device="cuda"), torch.empty(11, n // 8, device="cuda")
+        out = r if over == "residual" else x
+        fp8q.fp8q_rms_norm_quant(x, w, q=q, scale_inv=s, residual=r, residual_out=out, group=8)
+        assert torch.equal(out.double(), want_r)
+        P.check_groups(q, s, v, 8, 0, rel(n))
+
+
+def test_empty_calls_write_nothing(fp8q):
+    w = torch.ones(64, device="cuda")
+    x = torch.empty(0, 64, device="cuda")
+    q, s = fp8q.rms_norm_cast_to_fp8(x, w, group=32)
+    assert q.shape == (0, 64) and s.shape == (0, 2)
+    dw = torch.full((64,), 7.0, device="cuda")
+    fp8q.fp8q_rms_norm_bwd(x, x, w, torch.empty(0, device="cuda"), torch.empty_like(x), dw)
+    assert (dw == 0).all()
+    assert fp8q.rms_norm(torch.empty(3, 0, device="cuda"), torch.empty(0, device="cuda")).shape == (3, 0)
+
+
+# ---------------------------------------------------------------------------
+# backward
+# ---------------------------------------------------------------------------
+def check_backward(fp8q, m, n, dt, res, w32=False, offset=0):
+    x, r, w = make(m, n, dt, res, w32, seed=5)
+    g = torch.Generator(device="cuda").manual_seed(m + n)
+    dy = torch.randn(m, n, generator=g, device="cuda").to(dt)
+    dr = torch.randn(m, n, generator=g, device="cuda").to(dt) if res else None
+    r64, rstd64, _ = P.norm(x, w, r, EPS)
+    rows, rstd = r64.to(dt), rstd64.view(-1).float()
+    if offset:
+        rows, dy, w = shifted(rows, offset), shifted(dy, offset), shifted(w, offset)
+    dx, dw = Guarded(m * n, dt), Guarded(n, w.dtype)
+    ws = Guarded(fp8q.fp8q_rms_norm_bwd_workspace_bytes(m, n), torch.uint8)
+    fp8q.fp8q_rms_norm_bwd(dy, rows, w, rstd, dx.t.view(m, n), dw.t, ws.t, dr)
+    for b in (dx, dw, ws):
+        b.check()
+    want, want_w, mag, mag_w = P.norm_grad(r64, w, rstd64, dy, dr)
+    k = (max(32, n / 256) + 20) * P.U
+    tol = k * mag + want.abs() * P.half_step(dt) + P.tiny(dt)
+    assert ((dx.t.view(m, n).double() - want).abs() <= tol).all()
+    tol = (m + 64 + 4) * P.U * mag_w + want_w.abs() * P.half_step(w.dtype) + P.tiny(w.dtype)
+    assert ((dw.t.double() - want_w).abs() <= tol).all()
+    # without dweight, and again: the same bits
+    dx2 = torch.empty_like(dy)
+    fp8q.fp8q_rms_norm_bwd(dy, rows, w, rstd, dx2, dres=dr)
+    assert torch.equal(dx2.view(torch.uint8), dx.t.view(m, n).view(torch.uint8))
+    dw2 = torch.empty_like(w)
+    fp8q.fp8q_rms_norm_bwd(dy, rows, w, rstd, dx2, dw2, torch.empty_like(ws.t), dr)
+    assert torch.equal(dw2, dw.t)
+
+
+@pytest.mark.parametrize("dt", [BF16, F16, F32])
+@pytest.mark.parametrize("res", [False, True])
+@pytest.mark.parametrize("m,n", [(1, 64), (3, 7168), (1000, 128), (333, 1000), (7, 18432), (5, 20480), (2, 20488),
+                                 (40, 33), (2000, 1), (700, 4096), (1, 5)])
+def test_backward(fp8q, dt, res, m, n):
+    check_backward(fp8q, m, n, dt, res)
+
+
+@pytest.mark.parametrize("dt", [BF16, F16])
+@pytest.mark.parametrize("n", [2048, 999, 12288])
+def test_backward_fp32_weight(fp8q, dt, n):
+    check_backward(fp8q, 77, n, dt, True, w32=True)
+
+
+@pytest.mark.parametrize("dt,offset", [(BF16, 1), (F16, 4), (F32, 2)])
+def test_backward_unaligned(fp8q, dt, offset):
+    check_backward(fp8q, 50, 1024, dt, True, offset=offset)
+
+
+def test_gradient_against_differences(fp8q):
+    """The gradients along a random direction against central differences of the formula in 64
+    bits, whose own error is the step squared (1e-8) times third derivatives of order one."""
+    m, n = 6, 96
+    x, r, w = make(m, n, F32, True)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    dy, dr = torch.randn(m, n, generator=g, device="cuda"), torch.randn(m, n, generator=g, device="cuda")
+    for t in (x, r, w):
+        t.requires_grad_(True)
+    y, s = fp8q.rms_norm(x, w, residual=r)
+    gx, gr, gw = torch.autograd.grad((y, s), (x, r, w), (dy, dr))
+    assert torch.equal(gx, gr)
+
+    def loss(x, r, w):
+        z = x + r
+        v = z * (z.square().mean(1, keepdim=True) + EPS).rsqrt() * w
+        return (v * dy.double()).sum() + (z * dr.double()).sum()
+
+    for grad, i in ((gx, 0), (gr, 1), (gw, 2)):
+        args = [t.detach().double() for t in (x, r, w)]
+        d = torch.randn(args[i].shape, generator=g, device="cuda").double()
+        h = 1e-4
+        hi, lo = list(args), list(args)
+        hi[i], lo[i] = args[i] + h * d, args[i] - h * d
+        want = (loss(*hi) - loss(*lo)) / (2 * h)
+        got = (grad.double() * d).sum()
+        # r = x + residual is rounded to fp32 by the operator and not here: m n U of each term's size
+        scale = (grad.double() * d).abs().sum()
+        assert (got - want).abs() <= 64 * P.U * scale * 8 + 1e-5 * (1 + scale.sqrt())
+
+
+def test_autograd_uses_only_what_is_asked(fp8q):
+    x, r, w = make(9, 256, BF16, True)
+    x.requires_grad_(True)
+    y, s = fp8q.rms_norm(x, w, residual=r)
+    (gx,) = torch.autograd.grad(s, x, torch.ones_like(s), retain_graph=True)      # only the sum
+    assert torch.equal(gx, torch.ones_like(gx))
+    (gx,) = torch.autograd.grad(y, x, torch.ones_like(y))                          # only the norm
+    r64, rstd, _ = P.norm(x.detach(), w, r, EPS)
+    want, _, mag, _ = P.norm_grad(r64, w, rstd, torch.ones_like(y), None)
+    assert ((gx.double() - want).abs() <= 60 * P.U * mag + want.abs() * P.half_step(BF16)).all()
+    # a transposed input and leading dimensions
+    xt = torch.randn(256, 6, device="cuda").to(BF16).t()
+    z = fp8q.rms_norm(xt.reshape(2, 3, 256), w)
+    v = P.norm(xt.contiguous(), w, None, EPS)[2]
+    assert ((z.view(6, 256).double() - v).abs() <= v.abs() * (rel(256) + P.half_step(BF16))).all()
+
+
+def test_side_stream_and_graph_replay(fp8q):
+    """The forward and backward captured into a graph and replayed on new inputs give what the
+    eager calls give, bit for bit; a call inside a stream context runs on that stream."""
+    x, r, w = make(64, 1024, BF16, True)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    dy = torch.randn(64, 1024, generator=g, device="cuda").to(BF16)
+    q, s, ro = torch.empty(64, 1024, dtype=torch.uint8, device="cuda"), torch.empty(64, 8, device="cuda"), torch.empty_like(x)
+    rstd, dx, dw = torch.empty(64, device="cuda"), torch.empty_like(x), torch.empty_like(w)
+    ws = torch.empty(fp8q.fp8q_rms_norm_bwd_workspace_bytes(64, 1024), dtype=torch.uint8, device="cuda")
+
+    def step():
+        fp8q.fp8q_rms_norm_quant(x, w, q=q, scale_inv=s, residual=r, residual_out=ro, rstd=rstd)
+        fp8q.fp8q_rms_norm_bwd(dy, ro, w, rstd, dx, dw, ws)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+        graph = torch.cuda.CUDAGraph()
+        graph.capture_begin()
+        step()
+        graph.capture_end()
+    torch.cuda.current_stream().wait_stream(side)
+    x.copy_(make(64, 1024, BF16, False, seed=99)[0])
+    graph.replay()
+    got = [t.clone() for t in (q, s, ro, dx, dw)]
+    step()
+    for a, b in zip(got, (q, s, ro, dx, dw)):
+        assert torch.equal(a, b)
