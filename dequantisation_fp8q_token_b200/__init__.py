@@ -25,6 +25,8 @@ fp8 matrix products on the tensor cores (tcgen05):
 
 Norm and feed-forward operators (ffn.py):
     fp8q_rms_norm_quant, fp8q_rms_norm_bwd   residual addition, root-mean-square norm and fp8 cast
+    fp8q_gated_mm(_blockwise(_quant)), fp8q_gated_bwd_cast   both projections of a gated
+        feed-forward block, the activation and the product in one kernel, and its gradient
 
 Allocating helpers named after the functions on the pages:
     per_token_cast_to_fp8   (DeepEP "5 Utils")
@@ -175,6 +177,15 @@ def lib() -> ctypes.CDLL:
             L.fp8q_rms_norm_bwd_workspace_bytes.argtypes = [i64, i64]
             L.fp8q_rms_norm_bwd.restype = st
             L.fp8q_rms_norm_bwd.argtypes = [p, p, i32, p, i32, p, p, i64, i64, p, p, p, sz, p]
+            L.fp8q_gated_mm.restype = st
+            L.fp8q_gated_mm.argtypes = [p, i32, p, p, i32, i64, i64, i64, p, p, p, i32, i32, p, p, p, p]
+            L.fp8q_gated_mm_blockwise.restype = st
+            L.fp8q_gated_mm_blockwise.argtypes = [p, i32, p, p, p, p, p, i32, i64, i64, i64, i32, i32, p, p, p]
+            L.fp8q_gated_mm_blockwise_quant.restype = st
+            L.fp8q_gated_mm_blockwise_quant.argtypes = [p, i32, p, p, p, p, p, i32, i64, i64, i64, i32, i32, i32, p,
+                                                        p, p, p]
+            L.fp8q_gated_bwd_cast.restype = st
+            L.fp8q_gated_bwd_cast.argtypes = [p, p, i32, i64, i64, i32, i32, p, p, p, sz, i32, p]
             _lib = L
     return _lib
 

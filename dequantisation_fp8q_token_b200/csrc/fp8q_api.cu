@@ -544,3 +544,92 @@ fp8q_status fp8q_rms_norm_bwd(const void* dy, const void* r, fp8q_dtype xt, cons
 }
 
 }  // extern "C"
+
+namespace {
+
+bool act_ok(int a) { return a == FP8Q_ACT_SILU || a == FP8Q_ACT_GELU_TANH; }
+
+// shared checks of the gated products: those of the plain product with either
+// weight, then the caller's outputs; `yt` is any dtype where the output is codes
+fp8q_status check_gated(const GatedProblem& g, const void* out, bool* nothing) {
+    *nothing = false;
+    if (!act_ok(g.act)) return FP8Q_ERR_BAD_SHAPE;
+    fp8q_status st = check_scaled_mm(g.a, g.fa, g.w_gate, g.fb, g.M, g.I, g.K, g.sa, g.s_gate, nullptr, g.yt, out,
+                                     g.status, nothing);
+    if (st != FP8Q_OK) return st;
+    // gate_up has rows of 2 I
+    if (checked_mul(checked_mul(g.M, g.I), 2LL * dtype_bytes(g.yt)) < 0) return FP8Q_ERR_BAD_SHAPE;
+    if (*nothing) return FP8Q_OK;
+    return check_scaled_mm(g.a, g.fa, g.w_up, g.fb, g.M, g.I, g.K, g.sa, g.s_up, nullptr, g.yt, out, g.status, nothing);
+}
+
+}  // namespace
+
+extern "C" {
+
+fp8q_status fp8q_gated_mm(const uint8_t* a, fp8q_format fa, const uint8_t* w_gate, const uint8_t* w_up,
+                          fp8q_format fb, int64_t M, int64_t I, int64_t K, const float* scale_a,
+                          const float* scale_gate, const float* scale_up, fp8q_activation act, fp8q_dtype yt, void* h,
+                          void* gate_up, uint32_t* status, fp8q_stream_t stream) {
+    const GatedProblem g = {a,   w_gate, w_up, fa, fb,      M,       I,       K,           scale_a,     scale_gate, scale_up,
+                            false, act,  yt,   h,  gate_up, nullptr, nullptr, FP8Q_E4M3FN, FP8Q_SCALE_IEEE, status};
+    bool nothing = false;
+    const fp8q_status st = check_gated(g, h, &nothing);
+    if (st != FP8Q_OK || nothing) return st;
+    // the per-tensor epilogue reads the scales even when K == 0
+    if (!scale_a || !scale_gate || !scale_up) return FP8Q_ERR_NULL_POINTER;
+    if (!aligned(scale_a, 4) || !aligned(scale_gate, 4) || !aligned(scale_up, 4) || !aligned(gate_up, dtype_bytes(yt)))
+        return FP8Q_ERR_MISALIGNED;
+    return launch_gated_mm(g, reinterpret_cast<cudaStream_t>(stream));
+}
+
+fp8q_status fp8q_gated_mm_blockwise(const uint8_t* a, fp8q_format fa, const float* scale_a, const uint8_t* w_gate,
+                                    const float* scale_gate, const uint8_t* w_up, const float* scale_up,
+                                    fp8q_format fb, int64_t M, int64_t I, int64_t K, fp8q_activation act,
+                                    fp8q_dtype yt, void* h, uint32_t* status, fp8q_stream_t stream) {
+    const GatedProblem g = {a,    w_gate, w_up, fa, fb,      M,       I,       K,           scale_a,     scale_gate, scale_up,
+                            true, act,    yt,   h,  nullptr, nullptr, nullptr, FP8Q_E4M3FN, FP8Q_SCALE_IEEE, status};
+    bool nothing = false;
+    const fp8q_status st = check_gated(g, h, &nothing);
+    if (st != FP8Q_OK || nothing) return st;
+    return launch_gated_mm(g, reinterpret_cast<cudaStream_t>(stream));
+}
+
+fp8q_status fp8q_gated_mm_blockwise_quant(const uint8_t* a, fp8q_format fa, const float* scale_a,
+                                          const uint8_t* w_gate, const float* scale_gate, const uint8_t* w_up,
+                                          const float* scale_up, fp8q_format fb, int64_t M, int64_t I, int64_t K,
+                                          fp8q_activation act, fp8q_format fmt, fp8q_scale_rule rule, uint8_t* q,
+                                          float* scale_inv, uint32_t* status, fp8q_stream_t stream) {
+    const GatedProblem g = {a,    w_gate, w_up,      fa,      fb,      M, I,         K,   scale_a, scale_gate, scale_up,
+                            true, act,    FP8Q_BF16, nullptr, nullptr, q, scale_inv, fmt, rule,    status};
+    if (!rule_ok(rule)) return FP8Q_ERR_BAD_RULE;
+    if (!fmt_ok(fmt)) return FP8Q_ERR_BAD_FORMAT;
+    bool nothing = false;
+    const fp8q_status st = check_gated(g, scale_inv, &nothing);
+    if (st != FP8Q_OK || nothing) return st;
+    if (!q) return FP8Q_ERR_NULL_POINTER;
+    if (!aligned(scale_inv, 4)) return FP8Q_ERR_MISALIGNED;
+    return launch_gated_mm(g, reinterpret_cast<cudaStream_t>(stream));
+}
+
+fp8q_status fp8q_gated_bwd_cast(const void* dh, const void* gate_up, fp8q_dtype xt, int64_t M, int64_t I,
+                                fp8q_activation act, fp8q_format fmt, uint8_t* q, float* scale_inv, void* workspace,
+                                size_t workspace_bytes, fp8q_scale_rule rule, fp8q_stream_t stream) {
+    if (!dtype_ok(xt)) return FP8Q_ERR_BAD_DTYPE;
+    if (!rule_ok(rule)) return FP8Q_ERR_BAD_RULE;
+    if (!fmt_ok(fmt)) return FP8Q_ERR_BAD_FORMAT;
+    if (M < 0 || I < 0 || I > 0x7FFFFFFFLL || !act_ok(act)) return FP8Q_ERR_BAD_SHAPE;
+    const int64_t numel = checked_mul(M, I);
+    if (numel < 0 || checked_mul(numel, 2LL * dtype_bytes(xt)) < 0) return FP8Q_ERR_BAD_SHAPE;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (!scale_inv) return FP8Q_ERR_NULL_POINTER;
+    if (!aligned(scale_inv, 4)) return FP8Q_ERR_MISALIGNED;
+    if (numel == 0) return launch_fill(scale_inv, 1, 1.0f, s);
+    if (!dh || !gate_up || !q) return FP8Q_ERR_NULL_POINTER;
+    if (!aligned(dh, dtype_bytes(xt)) || !aligned(gate_up, dtype_bytes(xt))) return FP8Q_ERR_MISALIGNED;
+    if (!workspace || workspace_bytes < kPerTensorWorkspaceBytes || !aligned(workspace, 16))
+        return FP8Q_ERR_WORKSPACE;
+    return launch_gated_bwd(dh, gate_up, xt, M, I, act, fmt, rule, q, scale_inv, static_cast<uint32_t*>(workspace), s);
+}
+
+}  // extern "C"

@@ -106,6 +106,34 @@ fp8q_status launch_rms_norm_bwd(const void* dy, const void* r, int xt, const voi
                                 const void* dres, int64_t m, int64_t n, void* dx, void* dw, float* part,
                                 cudaStream_t s);
 
+// gated feed-forward products (gated_mm.cu): validated arguments.  fine as for
+// launch_scaled_mm; exactly one of h and q (q: fine scales); gate_up: per-tensor
+// scales, or null.
+struct GatedProblem {
+    const uint8_t* a;
+    const uint8_t* w_gate;
+    const uint8_t* w_up;
+    int fa, fb;
+    int64_t M, I, K;
+    const float* sa;
+    const float* s_gate;
+    const float* s_up;
+    bool fine;
+    int act;
+    int yt;
+    void* h;
+    void* gate_up;
+    uint8_t* q;
+    float* sinv;
+    int fmt, rule;
+    uint32_t* status;
+};
+fp8q_status launch_gated_mm(const GatedProblem& g, cudaStream_t s);
+// its elementwise backward and per-tensor cast (gated_bwd.cu): gate_up [M][2 I] and dh
+// [M][I] of type xt -> q [M][2 I], sinv [1]; partials: kPerTensorWorkspaceBytes
+fp8q_status launch_gated_bwd(const void* dh, const void* gate_up, int xt, int64_t M, int64_t I, int act, int fmt,
+                             int rule, uint8_t* q, float* sinv, uint32_t* partials, cudaStream_t s);
+
 inline fp8q_status cuda_status(cudaError_t e) { return e == cudaSuccess ? FP8Q_OK : FP8Q_ERR_CUDA; }
 
 }  // namespace fp8q

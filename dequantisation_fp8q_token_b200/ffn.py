@@ -2,10 +2,14 @@
 
 Entry points with the C names (caller-provided outputs, nothing allocated):
     fp8q_rms_norm_quant, fp8q_rms_norm_bwd
+    fp8q_gated_mm, fp8q_gated_mm_blockwise, fp8q_gated_mm_blockwise_quant, fp8q_gated_bwd_cast
 
 Allocating helpers:
-    rms_norm               residual addition and root-mean-square norm (differentiable)
-    rms_norm_cast_to_fp8   the same with the result cast to 1 x G fp8 groups
+    rms_norm                     residual addition and root-mean-square norm (differentiable)
+    rms_norm_cast_to_fp8         the same with the result cast to 1 x G fp8 groups
+    gated_linear_fp8             act(x Wg^T) * (x Wu^T) with linear_fp8's casts (differentiable)
+    gated_linear_fp8_blockwise   the same on block-scaled weights
+    ffn_fp8, ffn_fp8_blockwise   the whole block: the gated products, then the down projection
 """
 from __future__ import annotations
 
@@ -14,12 +18,19 @@ from typing import Optional
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import (E4M3FN, SCALE_IEEE, _FMT_DTYPE, _check, _dev_ptr, _dtype_code, _fmt_of, _need, _rule_of, _stream, lib)
+from . import (E4M3FN, E5M2, K_MAJOR, MN_MAJOR, SCALE_IEEE, _FMT_DTYPE, _FP8_DTYPES, _check, _dev_ptr, _dtype_code,
+               _fmt_of, _need, _rule_of, _status_word, _stream, fp8q_cast_per_tensor_ex,
+               fp8q_cast_per_tensor_workspace_bytes, fp8q_scaled_mm_blockwise, fp8q_scaled_mm_ex, lib, linear_fp8,
+               per_token_cast_to_fp8)
 
 __all__ = [
     "fp8q_rms_norm_quant", "fp8q_rms_norm_bwd", "fp8q_rms_norm_bwd_workspace_bytes",
     "rms_norm", "rms_norm_cast_to_fp8",
+    "ACT_SILU", "ACT_GELU_TANH", "fp8q_gated_mm", "fp8q_gated_mm_blockwise", "fp8q_gated_mm_blockwise_quant",
+    "fp8q_gated_bwd_cast", "gated_linear_fp8", "gated_linear_fp8_blockwise", "ffn_fp8", "ffn_fp8_blockwise",
 ]
+
+ACT_SILU, ACT_GELU_TANH = 0, 1
 
 
 # ---------------------------------------------------------------------------
@@ -159,3 +170,219 @@ def rms_norm_cast_to_fp8(x: torch.Tensor, weight: torch.Tensor, residual: Option
     fp8q_rms_norm_quant(x, weight, q=q, scale_inv=s, residual=residual, residual_out=r, eps=eps, group=group, fmt=f,
                         rule=rule)
     return (q, s) if r is None else (q, s, r)
+
+
+# ---------------------------------------------------------------------------
+# gated feed-forward block
+# ---------------------------------------------------------------------------
+def _act_of(act) -> int:
+    if isinstance(act, str):
+        return {"silu": ACT_SILU, "gelu_tanh": ACT_GELU_TANH}[act]
+    return int(act)
+
+
+def _gated_operands(a, w_gate, w_up, fa, fb):
+    if a.dim() != 2 or w_gate.dim() != 2 or w_up.shape != w_gate.shape or a.shape[1] != w_gate.shape[1]:
+        raise ValueError(f"a must be [M, K], w_gate and w_up [I, K], got {tuple(a.shape)}, {tuple(w_gate.shape)} and "
+                         f"{tuple(w_up.shape)}")
+    M, K = a.shape
+    I = w_gate.shape[0]
+    if w_gate.dtype != w_up.dtype:
+        raise TypeError("w_gate and w_up must have one dtype")
+    _need(a, M * K, "a", byte=True)
+    _need(w_gate, I * K, "w_gate", byte=True)
+    fa = _fmt_of(fa) if fa is not None else _FP8_DTYPES.get(a.dtype, E4M3FN)
+    fb = _fmt_of(fb) if fb is not None else _FP8_DTYPES.get(w_gate.dtype, E4M3FN)
+    return M, I, K, fa, fb
+
+
+def fp8q_gated_mm(a: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, scale_a: torch.Tensor,
+                  scale_gate: torch.Tensor, scale_up: torch.Tensor, out: torch.Tensor,
+                  gate_up: Optional[torch.Tensor] = None, act=ACT_SILU, fa=None, fb=None,
+                  status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """out[M, I] = act(gate) * up with gate = a @ w_gate.t() and up = a @ w_up.t() of fp8 codes a [M, K],
+    w_gate and w_up [I, K] and per-tensor scales (fp32 [1] each).  gate_up: optional [M, 2 I] of out's
+    dtype that receives gate and up for fp8q_gated_bwd_cast.  act: "silu" or "gelu_tanh"."""
+    M, I, K, fa, fb = _gated_operands(a, w_gate, w_up, fa, fb)
+    dev = a.device
+    for t, name in ((scale_a, "scale_a"), (scale_gate, "scale_gate"), (scale_up, "scale_up")):
+        _need(t, 1, name, dtype=torch.float32)
+    _need(out, M * I, "out")
+    if gate_up is not None:
+        _need(gate_up, 2 * M * I, "gate_up", dtype=out.dtype)
+    _check(lib().fp8q_gated_mm(
+        _dev_ptr(a, "a"), fa, _dev_ptr(w_gate, "w_gate", dev), _dev_ptr(w_up, "w_up", dev), fb, M, I, K,
+        _dev_ptr(scale_a, "scale_a", dev), _dev_ptr(scale_gate, "scale_gate", dev), _dev_ptr(scale_up, "scale_up", dev),
+        _act_of(act), _dtype_code(out, "out"), _dev_ptr(out, "out", dev), _dev_ptr(gate_up, "gate_up", dev),
+        _dev_ptr(_status_word(status), "status", dev), _stream(stream, dev)), "fp8q_gated_mm")
+
+
+def _fine_scales(M, I, K, scale_a, scale_gate, scale_up):
+    kb, ib = -(-K // 128), -(-I // 128)
+    _need(scale_a, M * kb, "scale_a", dtype=torch.float32)
+    _need(scale_gate, ib * kb, "scale_gate", dtype=torch.float32)
+    _need(scale_up, ib * kb, "scale_up", dtype=torch.float32)
+    return ib
+
+
+def fp8q_gated_mm_blockwise(a: torch.Tensor, scale_a: torch.Tensor, w_gate: torch.Tensor, scale_gate: torch.Tensor,
+                            w_up: torch.Tensor, scale_up: torch.Tensor, out: torch.Tensor, act=ACT_SILU, fa=None,
+                            fb=None, status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """fp8q_gated_mm with fine-grained scales: scale_a [M, ceil(K/128)] per 1 x 128 group, scale_gate and
+    scale_up [ceil(I/128), ceil(K/128)] per 128 x 128 block."""
+    M, I, K, fa, fb = _gated_operands(a, w_gate, w_up, fa, fb)
+    dev = a.device
+    _fine_scales(M, I, K, scale_a, scale_gate, scale_up)
+    _need(out, M * I, "out")
+    _check(lib().fp8q_gated_mm_blockwise(
+        _dev_ptr(a, "a"), fa, _dev_ptr(scale_a, "scale_a", dev), _dev_ptr(w_gate, "w_gate", dev),
+        _dev_ptr(scale_gate, "scale_gate", dev), _dev_ptr(w_up, "w_up", dev), _dev_ptr(scale_up, "scale_up", dev), fb,
+        M, I, K, _act_of(act), _dtype_code(out, "out"), _dev_ptr(out, "out", dev),
+        _dev_ptr(_status_word(status), "status", dev), _stream(stream, dev)), "fp8q_gated_mm_blockwise")
+
+
+def fp8q_gated_mm_blockwise_quant(a: torch.Tensor, scale_a: torch.Tensor, w_gate: torch.Tensor,
+                                  scale_gate: torch.Tensor, w_up: torch.Tensor, scale_up: torch.Tensor,
+                                  q: torch.Tensor, scale_inv: torch.Tensor, act=ACT_SILU, fa=None, fb=None, fmt=E4M3FN,
+                                  rule=SCALE_IEEE, status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """fp8q_gated_mm_blockwise with the result cast, unrounded, to fp8 codes q [M, I] and scale_inv
+    [M, ceil(I/128)]: the activations of the fp8q_scaled_mm_blockwise that follows."""
+    M, I, K, fa, fb = _gated_operands(a, w_gate, w_up, fa, fb)
+    dev = a.device
+    ib = _fine_scales(M, I, K, scale_a, scale_gate, scale_up)
+    _need(q, M * I, "q", byte=True)
+    _need(scale_inv, M * ib, "scale_inv", dtype=torch.float32)
+    _check(lib().fp8q_gated_mm_blockwise_quant(
+        _dev_ptr(a, "a"), fa, _dev_ptr(scale_a, "scale_a", dev), _dev_ptr(w_gate, "w_gate", dev),
+        _dev_ptr(scale_gate, "scale_gate", dev), _dev_ptr(w_up, "w_up", dev), _dev_ptr(scale_up, "scale_up", dev), fb,
+        M, I, K, _act_of(act), _fmt_of(fmt), _rule_of(rule), _dev_ptr(q, "q", dev),
+        _dev_ptr(scale_inv, "scale_inv", dev), _dev_ptr(_status_word(status), "status", dev), _stream(stream, dev)),
+        "fp8q_gated_mm_blockwise_quant")
+
+
+def fp8q_gated_bwd_cast(dh: torch.Tensor, gate_up: torch.Tensor, q: torch.Tensor, scale_inv: torch.Tensor,
+                        workspace: torch.Tensor, act=ACT_SILU, fmt=E5M2, rule=SCALE_IEEE, stream=None) -> None:
+    """The gradients of gate and up from dh [M, I] and fp8q_gated_mm's gate_up [M, 2 I], cast with one
+    scale into codes q [M, 2 I] and scale_inv [1]; workspace as fp8q_cast_per_tensor's."""
+    if dh.dim() != 2 or gate_up.dim() != 2 or gate_up.shape != (dh.shape[0], 2 * dh.shape[1]):
+        raise ValueError(f"dh must be [M, I] and gate_up [M, 2 I], got {tuple(dh.shape)} and {tuple(gate_up.shape)}")
+    if gate_up.dtype != dh.dtype:
+        raise TypeError("dh and gate_up must have one dtype")
+    M, I = dh.shape
+    dev = dh.device
+    _need(q, 2 * M * I, "q", byte=True)
+    _need(scale_inv, 1, "scale_inv", dtype=torch.float32)
+    _check(lib().fp8q_gated_bwd_cast(
+        _dev_ptr(dh, "dh"), _dev_ptr(gate_up, "gate_up", dev), _dtype_code(dh, "dh"), M, I, _act_of(act), _fmt_of(fmt),
+        _dev_ptr(q, "q", dev), _dev_ptr(scale_inv, "scale_inv", dev), _dev_ptr(workspace, "workspace", dev),
+        workspace.numel() * workspace.element_size(), _rule_of(rule), _stream(stream, dev)), "fp8q_gated_bwd_cast")
+
+
+def _cast_workspace(device) -> torch.Tensor:
+    """A cast's workspace of the call's own: the caching allocator orders it by stream and by graph."""
+    return torch.empty(fp8q_cast_per_tensor_workspace_bytes(), dtype=torch.uint8, device=device)
+
+
+def _tensor_cast(t: torch.Tensor):
+    q = torch.empty(t.shape, dtype=torch.float8_e4m3fn, device=t.device)
+    s = torch.empty((1,), dtype=torch.float32, device=t.device)
+    fp8q_cast_per_tensor_ex(t, q, s, _cast_workspace(t.device), E4M3FN)
+    return q, s
+
+
+class _GatedLinearFp8(torch.autograd.Function):
+    """gated_linear_fp8: _LinearFp8's casts and products around the gated kernel and its gradient.
+    Saves the fp8 input and weight and gate and up in the input's dtype."""
+
+    @staticmethod
+    def forward(ctx, x, w, act):
+        if x.dtype not in (torch.bfloat16, torch.float16) or x.dtype != w.dtype:
+            raise TypeError("Only float16 and bfloat16 are allowed.")
+        if w.dim() != 2 or w.shape[0] % 16 or x.shape[-1] != w.shape[1] or w.shape[1] % 16:
+            raise ValueError(f"weight must be [2 I, K] with 2 I and K multiples of 16 and K the input's width, got "
+                             f"{tuple(w.shape)} for an input of {tuple(x.shape)}")
+        x, w = x.contiguous(), w.contiguous()
+        I, K = w.shape[0] // 2, w.shape[1]
+        x2 = x.reshape(-1, K)
+        x8, sx = _tensor_cast(x2)
+        w8, sw = _tensor_cast(w)
+        h = torch.empty((x2.shape[0], I), dtype=x.dtype, device=x.device)
+        gate_up = None
+        if ctx.needs_input_grad[0] or ctx.needs_input_grad[1]:
+            gate_up = torch.empty((x2.shape[0], 2 * I), dtype=x.dtype, device=x.device)
+        fp8q_gated_mm(x8, w8[:I], w8[I:], sx, sw, sw, h, gate_up, act)
+        ctx.act, ctx.x_shape = act, x.shape
+        ctx.save_for_backward(x8, w8, sx, sw, gate_up)
+        return h.reshape(*x.shape[:-1], I)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dh):
+        x8, w8, sx, sw, gate_up = ctx.saved_tensors
+        dh = dh.contiguous().reshape(-1, dh.shape[-1])
+        d8 = torch.empty(gate_up.shape, dtype=torch.float8_e5m2, device=dh.device)
+        sd = torch.empty((1,), dtype=torch.float32, device=dh.device)
+        fp8q_gated_bwd_cast(dh, gate_up, d8, sd, _cast_workspace(dh.device), ctx.act)
+        dx = dw = None
+        if ctx.needs_input_grad[0]:
+            # dx[T, K] = d[T, 2 I] @ w[2 I, K], one product over gate's and up's columns together
+            dx = torch.empty(x8.shape, dtype=dh.dtype, device=dh.device)
+            fp8q_scaled_mm_ex(d8, w8, sd, sw, dx, a_layout=K_MAJOR, b_layout=MN_MAJOR)
+            dx = dx.reshape(ctx.x_shape)
+        if ctx.needs_input_grad[1]:
+            # dw[2 I, K] = d^T[2 I, T] @ x[T, K]
+            dw = torch.empty(w8.shape, dtype=dh.dtype, device=dh.device)
+            fp8q_scaled_mm_ex(d8, x8, sd, sx, dw, a_layout=MN_MAJOR, b_layout=MN_MAJOR)
+        return dx, dw, None
+
+
+def gated_linear_fp8(input: torch.Tensor, weight: torch.Tensor, act="silu") -> torch.Tensor:
+    """act(input @ Wg.t()) * (input @ Wu.t()) for weight = [Wg; Wu] of shape [2 I, K] (fp16 or bf16), with
+    linear_fp8's per-tensor e4m3 casts of input and weight; differentiable, the gradients of gate and
+    up cast together to e5m2.  The output has the input's dtype and last dimension I."""
+    return _GatedLinearFp8.apply(input, weight, _act_of(act))
+
+
+def gated_linear_fp8_blockwise(input: torch.Tensor, w_gate: torch.Tensor, scale_gate: torch.Tensor,
+                               w_up: torch.Tensor, scale_up: torch.Tensor, act="silu") -> torch.Tensor:
+    """act(input @ w_gate.t()) * (input @ w_up.t()) on fp8 weights [I, K] with 128 x 128 block scales: the
+    input is quantised per token, as linear_fp8_blockwise does; the output has the input's dtype."""
+    x = input.contiguous().reshape(-1, input.shape[-1])
+    q, s = per_token_cast_to_fp8(x)
+    h = torch.empty((x.shape[0], w_gate.shape[0]), dtype=input.dtype, device=input.device)
+    fp8q_gated_mm_blockwise(q, s, w_gate, scale_gate, w_up, scale_up, h, act)
+    return h.reshape(*input.shape[:-1], w_gate.shape[0])
+
+
+def ffn_fp8(input: torch.Tensor, w_gate_up: torch.Tensor, w_down: torch.Tensor, act="silu") -> torch.Tensor:
+    """A gated feed-forward block with per-tensor fp8 casts, differentiable:
+    linear_fp8(gated_linear_fp8(input, w_gate_up), w_down)."""
+    return linear_fp8(gated_linear_fp8(input, w_gate_up, act), w_down)
+
+
+def ffn_fp8_blockwise(input: torch.Tensor, w_gate: torch.Tensor, scale_gate: torch.Tensor, w_up: torch.Tensor,
+                      scale_up: torch.Tensor, w_down: torch.Tensor, scale_down: torch.Tensor,
+                      norm_weight: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
+                      eps: float = 1e-6, act="silu"):
+    """A gated feed-forward block on fp8 weights with 128 x 128 block scales, three launches from the
+    input to the output: (with norm_weight) the residual's addition, the norm and its cast; the gated
+    products and the cast of their result; the down projection w_down [N, I].  Returns the output in
+    the input's dtype, or (output, input + residual) when a residual is given."""
+    x = input.contiguous().reshape(-1, input.shape[-1])
+    r = None
+    if norm_weight is None:
+        if residual is not None:
+            raise ValueError("a residual needs norm_weight")
+        q, s = per_token_cast_to_fp8(x)
+    elif residual is None:
+        q, s = rms_norm_cast_to_fp8(x, norm_weight, eps=eps)
+    else:
+        q, s, r = rms_norm_cast_to_fp8(x, norm_weight, residual.reshape(x.shape), eps)
+    M, I = x.shape[0], w_gate.shape[0]
+    h = torch.empty((M, I), dtype=torch.float8_e4m3fn, device=x.device)
+    sh = torch.empty((M, -(-I // 128)), dtype=torch.float32, device=x.device)
+    fp8q_gated_mm_blockwise_quant(q, s, w_gate, scale_gate, w_up, scale_up, h, sh, act)
+    out = torch.empty((M, w_down.shape[0]), dtype=input.dtype, device=x.device)
+    fp8q_scaled_mm_blockwise(h, sh, w_down, scale_down, out)
+    out = out.reshape(*input.shape[:-1], w_down.shape[0])
+    return out if r is None else (out, r.reshape(input.shape))

@@ -27,6 +27,10 @@
  *   fp8q_*_ex                   torch's rounding of the scale expressions
  *   fp8q_rms_norm_quant, _bwd   residual addition, root-mean-square norm and
  *                               the cast of its result; its gradient
+ *   fp8q_gated_mm,              both projections of a gated feed-forward block,
+ *   fp8q_gated_mm_blockwise,    the activation and the product (per-tensor or
+ *   _blockwise_quant,           fine-grained scales, the latter with an fp8
+ *   fp8q_gated_bwd_cast         result); the elementwise part of the gradient
  *   fp8q_scaled_mm_wait_test,   tests of the products' bounded waits
  *   fp8q_scaled_mm_blockwise_wait_test
  *
@@ -569,6 +573,68 @@ size_t fp8q_rms_norm_bwd_workspace_bytes(int64_t m, int64_t n);
 fp8q_status fp8q_rms_norm_bwd(const void* dy, const void* r, fp8q_dtype xt, const void* weight, fp8q_dtype wt,
                               const float* rstd, const void* dres, int64_t m, int64_t n, void* dx, void* dweight,
                               void* workspace, size_t workspace_bytes, fp8q_stream_t stream);
+
+/*
+ * The first half of a gated feed-forward block in one kernel: both
+ * projections, the activation and the product.
+ *   gate = a Wg^T, up = a Wu^T        (fp8 products, as fp8q_scaled_mm(_blockwise))
+ *   h    = act(gate) * up             act(g) = g * sigmoid(p(g))
+ *     FP8Q_ACT_SILU       p(g) = g
+ *     FP8Q_ACT_GELU_TANH  p(g) = 2 sqrt(2 / pi) (g + 0.044715 g^3)
+ * gate and up stay fp32 until h is rounded, once.  act(-Inf) is NaN, as in
+ * torch.
+ */
+typedef enum { FP8Q_ACT_SILU = 0, FP8Q_ACT_GELU_TANH = 1 } fp8q_activation;
+
+/*
+ * With per-tensor scales: gate = acc * fl(scale_a * scale_gate), up likewise.
+ * a: [M][K] codes (format fa); w_gate, w_up: [I][K] codes (format fb), row-major.
+ * h: [M][I] of type yt.  gate_up: NULL, or [M][2 I] of type yt, which receives
+ *   gate (columns 0 .. I - 1) and up (I .. 2 I - 1), rounded, for the backward
+ *   pass; h is computed from the unrounded values.
+ * scale_*: device fp32 [1] each.  status and errors as fp8q_scaled_mm (K % 16,
+ *   16-byte aligned a, w_gate and w_up); an unknown act -> FP8Q_ERR_BAD_SHAPE.
+ */
+fp8q_status fp8q_gated_mm(const uint8_t* a, fp8q_format fa, const uint8_t* w_gate, const uint8_t* w_up,
+                          fp8q_format fb, int64_t M, int64_t I, int64_t K, const float* scale_a,
+                          const float* scale_gate, const float* scale_up, fp8q_activation act, fp8q_dtype yt, void* h,
+                          void* gate_up, uint32_t* status, fp8q_stream_t stream);
+
+/*
+ * With fine-grained scales: scale_a fp32 [M][ceil(K/128)] per 1 x 128 group,
+ * scale_gate and scale_up fp32 [ceil(I/128)][ceil(K/128)] per 128 x 128 block,
+ * folded as fp8q_scaled_mm_blockwise does.  h: [M][I] of type yt.
+ */
+fp8q_status fp8q_gated_mm_blockwise(const uint8_t* a, fp8q_format fa, const float* scale_a, const uint8_t* w_gate,
+                                    const float* scale_gate, const uint8_t* w_up, const float* scale_up,
+                                    fp8q_format fb, int64_t M, int64_t I, int64_t K, fp8q_activation act,
+                                    fp8q_dtype yt, void* h, uint32_t* status, fp8q_stream_t stream);
+
+/*
+ * The same with the result cast, unrounded, to 1 x 128 groups: q [M][I] codes
+ * of format fmt and scale_inv fp32 [M][ceil(I/128)], under the rules of
+ * fp8q_per_token_group_quant_ex.  When I is not a multiple of 128 the last
+ * group of a row is the rest of it.  q and scale_inv are the activations of the
+ * fp8q_scaled_mm_blockwise that follows (for which I % 16 == 0).
+ */
+fp8q_status fp8q_gated_mm_blockwise_quant(const uint8_t* a, fp8q_format fa, const float* scale_a,
+                                          const uint8_t* w_gate, const float* scale_gate, const uint8_t* w_up,
+                                          const float* scale_up, fp8q_format fb, int64_t M, int64_t I, int64_t K,
+                                          fp8q_activation act, fp8q_format fmt, fp8q_scale_rule rule, uint8_t* q,
+                                          float* scale_inv, uint32_t* status, fp8q_stream_t stream);
+
+/*
+ * The elementwise part of the backward pass, cast for the products after it:
+ *   s = sigmoid(p(gate))
+ *   d_gate = dh * up * s * (1 + gate * (1 - s) * p'(gate)),  d_up = dh * gate * s
+ *   q [M][2 I], scale_inv [1]: fp8q_cast_per_tensor_ex of [d_gate | d_up] (fp32,
+ *   not rounded in between; a zero or NaN amax is replaced by 1)
+ * dh: [M][I] and gate_up: [M][2 I] of type xt, as fp8q_gated_mm wrote it.
+ * workspace: as fp8q_cast_per_tensor.  M * I == 0: scale_inv[0] = 1.
+ */
+fp8q_status fp8q_gated_bwd_cast(const void* dh, const void* gate_up, fp8q_dtype xt, int64_t M, int64_t I,
+                                fp8q_activation act, fp8q_format fmt, uint8_t* q, float* scale_inv, void* workspace,
+                                size_t workspace_bytes, fp8q_scale_rule rule, fp8q_stream_t stream);
 
 #ifdef __cplusplus
 }

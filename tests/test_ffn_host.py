@@ -73,3 +73,94 @@ def test_host_tensors_and_wrong_shapes_are_refused(L):
             call()
     with pytest.raises(TypeError):
         f.fp8q_rms_norm_quant(x, w, y=x.float())
+
+
+def test_gated_validation(L):
+    def f(a=A, fa=0, wg=A, wu=A, fb=0, M=4, I=32, K=64, sa=P, sg=P, su=P, act=0, yt=2, h=P, gu=None, st=None):
+        return L.fp8q_gated_mm(a, fa, wg, wu, fb, M, I, K, sa, sg, su, act, yt, h, gu, st, None)
+
+    def b(a=A, fa=0, wg=A, wu=A, fb=0, M=4, I=32, K=64, sa=P, sg=P, su=P, act=0, yt=2, h=P, st=None):
+        return L.fp8q_gated_mm_blockwise(a, fa, sa, wg, sg, wu, su, fb, M, I, K, act, yt, h, st, None)
+
+    def q(a=A, fa=0, wg=A, wu=A, fb=0, M=4, I=32, K=64, sa=P, sg=P, su=P, act=0, fmt=0, rule=0, h=P, sinv=P, st=None):
+        return L.fp8q_gated_mm_blockwise_quant(a, fa, sa, wg, sg, wu, su, fb, M, I, K, act, fmt, rule, h, sinv, st, None)
+
+    for c in (f, b, q):
+        assert c(act=2) == 4 and c(act=-1) == 4                                   # unknown activation
+        assert c(fa=2) == 3 and c(fb=7) == 3
+        assert c(K=24) == 4 and c(M=-1) == 4 and c(I=-1) == 4 and c(I=1 << 31) == 4
+        assert c(a=None) == 1 and c(wg=None) == 1 and c(wu=None) == 1 and c(h=None) == 1
+        assert c(sa=None) == 1 and c(sg=None) == 1 and c(su=None) == 1
+        assert c(a=A + 8) == 5 and c(wg=A + 8) == 5 and c(wu=A + 8) == 5
+        assert c(sa=P + 2) == 5 and c(sg=P + 2) == 5 and c(su=P + 2) == 5 and c(st=P + 2) == 5
+        assert c(M=0, a=None, h=None) == 0 and c(I=0, wg=None, wu=None, h=None) == 0
+    assert f(yt=5) == 2 and b(yt=5) == 2
+    assert f(h=P + 1) == 5 and b(h=P + 1) == 5 and f(gu=P + 1) == 5
+    assert f(K=0, sa=None) == 1                                                   # the epilogue reads the scales
+    assert q(fmt=3) == 3 and q(rule=2) == 10
+    assert q(sinv=None) == 1 and q(sinv=P + 2) == 5
+
+
+def test_gated_bwd_validation(L):
+    ws = 8192
+
+    def f(dh=P, gu=P, xt=2, M=4, I=32, act=0, fmt=1, q=P, s=P, w=A, nb=ws, rule=0):
+        return L.fp8q_gated_bwd_cast(dh, gu, xt, M, I, act, fmt, q, s, w, nb, rule, None)
+    assert f(xt=4) == 2 and f(rule=3) == 10 and f(fmt=2) == 3
+    assert f(M=-1) == 4 and f(I=-1) == 4 and f(act=5) == 4 and f(M=1 << 62, I=4) == 4
+    assert f(s=None) == 1 and f(dh=None) == 1 and f(gu=None) == 1 and f(q=None) == 1
+    assert f(s=P + 2) == 5 and f(dh=P + 1) == 5 and f(gu=P + 1) == 5
+    assert f(w=None) == 6 and f(nb=ws - 1) == 6 and f(w=A + 8) == 6
+
+
+def test_gated_binding_refuses(L):
+    import dequantisation_fp8q_token_b200 as f
+    e4 = torch.float8_e4m3fn
+    a, w, w2 = torch.zeros(4, 256, dtype=e4), torch.zeros(64, 256, dtype=e4), torch.zeros(32, 256, dtype=e4)
+    sa, sw, one = torch.ones(4, 2), torch.ones(1, 2), torch.ones(1)
+    h, gu = torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(4, 128, dtype=torch.bfloat16)
+    q, s = torch.zeros(4, 64, dtype=e4), torch.zeros(4, 1)
+    ws = torch.zeros(8192, dtype=torch.uint8)
+    x, wx = torch.zeros(4, 256, dtype=torch.bfloat16), torch.zeros(64, 256, dtype=torch.bfloat16)
+    for call in (lambda: f.fp8q_gated_mm(a, w, w, one, one, one, h, gu),
+                 lambda: f.fp8q_gated_mm_blockwise(a, sa, w, sw, w, sw, h),
+                 lambda: f.fp8q_gated_mm_blockwise_quant(a, sa, w, sw, w, sw, q, s),
+                 lambda: f.fp8q_gated_bwd_cast(h, gu, torch.zeros(4, 128, dtype=torch.uint8), one, ws),
+                 lambda: f.gated_linear_fp8(x, wx), lambda: f.ffn_fp8(x, wx, torch.zeros(256, 32, dtype=torch.bfloat16)),
+                 lambda: f.gated_linear_fp8_blockwise(x, w, sw, w, sw),
+                 lambda: f.ffn_fp8_blockwise(x, w, sw, w, sw, torch.zeros(256, 64, dtype=e4), torch.ones(2, 1))):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
+    for call in (lambda: f.fp8q_gated_mm(a, w, w2, one, one, one, h),                     # I differs
+                 lambda: f.fp8q_gated_mm(a, w[:, :128], w[:, :128], one, one, one, h),    # K differs
+                 lambda: f.fp8q_gated_mm(a, w, w, one, one, one, h[:2]),                  # out too small
+                 lambda: f.fp8q_gated_mm(a, w, w, one, one, one, h, gu[:2]),              # gate_up too small
+                 lambda: f.fp8q_gated_mm_blockwise(a, sa[:2], w, sw, w, sw, h),           # scales too few
+                 lambda: f.fp8q_gated_mm_blockwise(a, sa, w, sw[:, :1], w, sw, h),
+                 lambda: f.fp8q_gated_mm_blockwise_quant(a, sa, w, sw, w, sw, q, s[:2]),
+                 lambda: f.fp8q_gated_bwd_cast(h, h, q, one, ws),                         # gate_up's width
+                 lambda: f.gated_linear_fp8(x, wx[:, :128]), lambda: f.gated_linear_fp8(x, wx[:40]),
+                 lambda: f.ffn_fp8_blockwise(x, w, sw, w, sw, w, sw, residual=x)):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: f.fp8q_gated_mm(a, w, w.view(torch.float8_e5m2), one, one, one, h),
+                 lambda: f.fp8q_gated_mm(a.float(), w, w, one, one, one, h),
+                 lambda: f.fp8q_gated_mm(a, w, w, one, one, one, h, gu.float()),
+                 lambda: f.gated_linear_fp8(x.float(), wx.float()), lambda: f.gated_linear_fp8(x, wx.half())):
+        with pytest.raises(TypeError):
+            call()
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+def test_the_plain_derivative_is_that_of_differences(act):
+    """The 64-bit activation that the GPU tests compare with: value against its definition as
+    g * sigmoid(p(g)), derivative against central differences (error: the step squared)."""
+    import plain64
+    g = torch.linspace(-12, 12, 4001, dtype=torch.float64)
+    v, d = plain64.act(g, act)
+    p, dp = plain64.exponent(g, act)
+    s = torch.sigmoid(p)
+    assert (v - g * s).abs().max() < 1e-13
+    assert (d - s * (1 + g * (1 - s) * dp)).abs().max() < 1e-12
+    h = 1e-5
+    assert (d - (plain64.act(g + h, act)[0] - plain64.act(g - h, act)[0]) / (2 * h)).abs().max() < 1e-9
