@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "fp8q.h"
 
 #ifndef FP8Q_PDL
@@ -18,6 +20,18 @@ constexpr size_t kPerTensorWorkspaceBytes = kMaxPartials * sizeof(uint32_t);
 
 // number of SMs of the current device (cached per device)
 int sm_count();
+
+// Allow `kernel` `bytes` of dynamic shared memory, asked of the runtime once per device (`done`: a
+// static array of the caller's, one per kernel).
+template <typename Kernel>
+cudaError_t allow_smem(Kernel kernel, int bytes, std::atomic<bool> (&done)[64]) {
+    int dev = -1;
+    const bool known = cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64;
+    if (known && done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && known) done[dev].store(true, std::memory_order_relaxed);
+    return e;
+}
 
 // CTAs of `kernel` with `threads` threads that fit on one SM at once (>= 1)
 template <typename Kernel>

@@ -21,32 +21,42 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// gradients of gate and up for one element.  1 - s is taken where it keeps its
-// digits; where s (1 - s) is 0 the curvature term is 0 whatever p' is.
-__device__ __forceinline__ void gated_grad(float dh, float g, float u, int act, float& dg, float& du) {
-    float p = g, dp = 1.0f;
-    if (act != FP8Q_ACT_SILU) {
-        const float g2 = __fmul_rn(g, g);
-        p = __fmul_rn(__fmul_rn(1.5957691216057308f, g), __fmaf_rn(0.044715f, g2, 1.0f));
-        dp = __fmul_rn(1.5957691216057308f, __fmaf_rn(0.134145f, g2, 1.0f));
+// Gradients of gate and up for two elements, in packed fp32 operations where
+// there are any (half the issue slots; the two MUFU operations an element are
+// what is left).  With a = gate * s, act' = s + a (1 - s) p'.  1 - s is 0 where
+// |p| is large, so p' takes a capped square, which cannot overflow.
+template <bool GELU>
+__device__ __forceinline__ void gated_grad2(float2 dh, float2 g, float2 u, float2& dg, float2& du) {
+    float2 s, om;
+    if constexpr (GELU) s = make_float2(sigmoid_approx(gelu_exponent(g.x)), sigmoid_approx(gelu_exponent(g.y)));
+    else s = make_float2(sigmoid_approx(g.x), sigmoid_approx(g.y));
+    const float2 a = __fmul2_rn(g, s);
+    om = __ffma2_rn(s, make_float2(-1.0f, -1.0f), make_float2(1.0f, 1.0f));
+    if constexpr (GELU) {
+        const float2 g2 = __fmul2_rn(g, g);
+        const float2 dp = __ffma2_rn(make_float2(fminf(g2.x, 1e12f), fminf(g2.y, 1e12f)),
+                                     make_float2(0.2140644488f, 0.2140644488f),        // 2 sqrt(2/pi) * 3 * 0.044715
+                                     make_float2(1.5957691216f, 1.5957691216f));
+        om = __fmul2_rn(om, dp);
     }
-    const float e = __expf(-p);
-    const float s = __fdividef(1.0f, __fadd_rn(1.0f, e));
-    const float om = e < 1.0f ? __fmul_rn(e, s) : __fsub_rn(1.0f, s);
-    const float so = __fmul_rn(s, om);
-    const float d = so == 0.0f ? s : __fmaf_rn(__fmul_rn(g, so), dp, s);
-    dg = __fmul_rn(__fmul_rn(dh, u), d);
-    du = __fmul_rn(dh, __fmul_rn(g, s));
+    dg = __fmul2_rn(__fmul2_rn(dh, u), __ffma2_rn(a, om, s));
+    du = __fmul2_rn(dh, a);
+}
+// magnitude maximum of three values, keeping NaN
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+    float d;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
 }
 
 template <int XT, int VB> struct Elems { static constexpr int N = VB / ElemBytes<XT>::value; };
+// pair i of a vector
 template <int XT, int VB>
-__device__ __forceinline__ void widen(const Vec<VB>& v, float (&f)[Elems<XT, VB>::N]) {
-#pragma unroll
-    for (int i = 0; i < VB / 4; ++i) {
-        if constexpr (XT == kF32) f[i] = __uint_as_float(v.w[i]);
-        else widen2<XT>(v.w[i], f[2 * i], f[2 * i + 1]);
-    }
+__device__ __forceinline__ float2 pair_of(const Vec<VB>& v, int i) {
+    if constexpr (XT == kF32) return make_float2(__uint_as_float(v.w[2 * i]), __uint_as_float(v.w[2 * i + 1]));
+    float2 f;
+    if constexpr (XT != kF32) widen2<XT>(v.w[i], f.x, f.y);
+    return f;
 }
 
 struct BwdArgs {
@@ -64,7 +74,7 @@ __device__ __forceinline__ void place(const BwdArgs& a, int64_t v, int epv, int6
     e_gate = e_dh + row * a.I;
 }
 
-template <int XT, int VB>
+template <int XT, int VB, bool GELU>
 __global__ void __launch_bounds__(kThreads)
 gated_amax_kernel(const BwdArgs a, uint32_t* __restrict__ partials) {
     constexpr int ES = ElemBytes<XT>::value, N = Elems<XT, VB>::N;
@@ -73,28 +83,25 @@ gated_amax_kernel(const BwdArgs a, uint32_t* __restrict__ partials) {
     // vectors from keep_from on stay in L2 for pass 2 (three streams)
     const int64_t keep_from = a.nvec - kL2KeepBytes / (3 * VB);
     const uint64_t keep = l2_evict_last_policy(), drop = l2_evict_first_policy();
-    uint32_t m = 0u;
+    float m = 0.0f;
     for (int64_t v = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; v < a.nvec;
          v += static_cast<int64_t>(gridDim.x) * kThreads) {
         int64_t ed, eg;
         place(a, v, N, ed, eg);
         const uint64_t pol = v >= keep_from ? keep : drop;
-        float d[N], g[N], u[N];
         const Vec<VB> vd = load_vec_policy<VB>(a.dh + ed * ES, pol);
         const Vec<VB> vg = load_vec_policy<VB>(a.gu + eg * ES, pol);
         const Vec<VB> vu = load_vec_policy<VB>(a.gu + (eg + a.I) * ES, pol);
-        widen<XT, VB>(vd, d);
-        widen<XT, VB>(vg, g);
-        widen<XT, VB>(vu, u);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            float dg, du;
-            gated_grad(d[i], g[i], u[i], a.act, dg, du);
-            m = max(m, max(__float_as_uint(dg) & 0x7FFFFFFFu, __float_as_uint(du) & 0x7FFFFFFFu));
+        for (int i = 0; i < N / 2; ++i) {
+            float2 dg, du;
+            gated_grad2<GELU>(pair_of<XT, VB>(vd, i), pair_of<XT, VB>(vg, i), pair_of<XT, VB>(vu, i), dg, du);
+            m = max3_abs(m, dg.x, du.x);
+            m = max3_abs(m, dg.y, du.y);
         }
     }
-    m = block_max_u32(m, sh);
-    if (threadIdx.x == 0) partials[blockIdx.x] = m;
+    const uint32_t bits = block_max_u32(__float_as_uint(m) & 0x7FFFFFFFu, sh);
+    if (threadIdx.x == 0) partials[blockIdx.x] = bits;
 }
 
 template <int N, int FMT, bool FIX>
@@ -111,7 +118,7 @@ __device__ __forceinline__ void encode_vec(const float (&v)[N], float scale, uin
     else st_u32(dst, c[0]);
 }
 
-template <int XT, int FMT, int VB>
+template <int XT, int FMT, int VB, bool GELU>
 __global__ void __launch_bounds__(kThreads)
 gated_cast_kernel(const BwdArgs a, const uint32_t* __restrict__ partials, int nparts, uint8_t* __restrict__ q,
                   float* __restrict__ sinv, int rule) {
@@ -127,19 +134,18 @@ gated_cast_kernel(const BwdArgs a, const uint32_t* __restrict__ partials, int np
          t += static_cast<int64_t>(gridDim.x) * kThreads) {
         int64_t ed, eg;
         place(a, a.nvec - 1 - t, N, ed, eg);
-        float d[N], g[N], u[N];
         const Vec<VB> vd = load_vec_policy<VB>(a.dh + ed * ES, drop);
         const Vec<VB> vg = load_vec_policy<VB>(a.gu + eg * ES, drop);
         const Vec<VB> vu = load_vec_policy<VB>(a.gu + (eg + a.I) * ES, drop);
-        widen<XT, VB>(vd, d);
-        widen<XT, VB>(vg, g);
-        widen<XT, VB>(vu, u);
+        float g[N], u[N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            float dg, du;
-            gated_grad(d[i], g[i], u[i], a.act, dg, du);
-            g[i] = dg;
-            u[i] = du;
+        for (int i = 0; i < N / 2; ++i) {
+            float2 dg, du;
+            gated_grad2<GELU>(pair_of<XT, VB>(vd, i), pair_of<XT, VB>(vg, i), pair_of<XT, VB>(vu, i), dg, du);
+            g[2 * i] = dg.x;
+            g[2 * i + 1] = dg.y;
+            u[2 * i] = du.x;
+            u[2 * i + 1] = du.y;
         }
         if (!fix) {
             encode_vec<N, FMT, false>(g, scale, q + eg);
@@ -152,6 +158,13 @@ gated_cast_kernel(const BwdArgs a, const uint32_t* __restrict__ partials, int np
 }
 
 // any width, element-aligned pointers: one element at a time, both passes
+__device__ __forceinline__ void gated_grad(float dh, float g, float u, int act, float& dg, float& du) {
+    float2 a, b;
+    if (act == FP8Q_ACT_SILU) gated_grad2<false>(make_float2(dh, 0.0f), make_float2(g, 0.0f), make_float2(u, 0.0f), a, b);
+    else gated_grad2<true>(make_float2(dh, 0.0f), make_float2(g, 0.0f), make_float2(u, 0.0f), a, b);
+    dg = a.x;
+    du = b.x;
+}
 template <int XT>
 __global__ void __launch_bounds__(kThreads)
 gated_amax_generic_kernel(const BwdArgs a, int64_t numel, uint32_t* __restrict__ partials) {
@@ -199,14 +212,14 @@ int grid_for(int64_t items) {
     return static_cast<int>(want < most ? want : most);
 }
 
-template <int XT, int FMT, int VB>
+template <int XT, int FMT, int VB, bool GELU>
 fp8q_status run_vec(BwdArgs a, int64_t numel, uint8_t* q, float* sinv, uint32_t* partials, int rule, cudaStream_t s) {
     a.nvec = numel / Elems<XT, VB>::N;
     a.vpr = static_cast<uint32_t>(a.I / Elems<XT, VB>::N);
     const int grid = grid_for(a.nvec);
-    cudaError_t e = launch_kernel(gated_amax_kernel<XT, VB>, dim3(grid), dim3(kThreads), s, a, partials);
+    cudaError_t e = launch_kernel(gated_amax_kernel<XT, VB, GELU>, dim3(grid), dim3(kThreads), s, a, partials);
     if (e != cudaSuccess) return cuda_status(e);
-    return cuda_status(launch_kernel(gated_cast_kernel<XT, FMT, VB>, dim3(grid), dim3(kThreads), s, a,
+    return cuda_status(launch_kernel(gated_cast_kernel<XT, FMT, VB, GELU>, dim3(grid), dim3(kThreads), s, a,
                                      static_cast<const uint32_t*>(partials), grid, q, sinv, rule));
 }
 
@@ -217,8 +230,13 @@ fp8q_status run(const BwdArgs& a, int64_t numel, uint8_t* q, float* sinv, uint32
         return a.I % (vb / ES) == 0 && reinterpret_cast<uintptr_t>(a.dh) % vb == 0 &&
                reinterpret_cast<uintptr_t>(a.gu) % vb == 0 && reinterpret_cast<uintptr_t>(q) % (vb / ES) == 0;
     };
-    if (fits(32)) return run_vec<XT, FMT, 32>(a, numel, q, sinv, partials, rule, s);
-    if (fits(16)) return run_vec<XT, FMT, 16>(a, numel, q, sinv, partials, rule, s);
+    const bool gelu = a.act == FP8Q_ACT_GELU_TANH;
+    if (fits(32))
+        return gelu ? run_vec<XT, FMT, 32, true>(a, numel, q, sinv, partials, rule, s)
+                    : run_vec<XT, FMT, 32, false>(a, numel, q, sinv, partials, rule, s);
+    if (fits(16))
+        return gelu ? run_vec<XT, FMT, 16, true>(a, numel, q, sinv, partials, rule, s)
+                    : run_vec<XT, FMT, 16, false>(a, numel, q, sinv, partials, rule, s);
     const int grid = grid_for(numel);
     cudaError_t e = launch_kernel(gated_amax_generic_kernel<XT>, dim3(grid), dim3(kThreads), s, a, numel, partials);
     if (e != cudaSuccess) return cuda_status(e);

@@ -25,7 +25,6 @@
 //   gated_pair_kernel             per-tensor scales, many tiles: 256 rows on
 //     CTA pairs (tcgen05.mma.cta_group::2), the even CTA loading the tile's
 //     rows of Wg and the odd one its rows of Wu.
-#include <atomic>
 #include <cstring>
 
 #include "mm_device.cuh"
@@ -58,7 +57,7 @@ struct GatedParams {
     uint8_t* q;                 // [M][I] codes
     float* sinv;                // [M][ceil(I/128)]
     int groups;                 // ceil(I/128)
-    int vec_h, vec_gu, vec_q;   // rows 32-byte aligned (base, pitch and up's offset)
+    int align_h, align_gu, align_q;   // 32, 16 or 1: what bases and row pitches (and up's offset) are multiples of
     int fmt, rule;              // of the codes
     int act;
     int stage_tx;               // bytes one stage's TMA boxes bring
@@ -67,14 +66,12 @@ struct GatedParams {
     uint64_t wait_limit_ns;
 };
 
-// act(g) * u.  The sigmoid's quotient is taken in one step, g / (1 + e^-p):
-// e^-p overflows to Inf for p below -88, where the quotient is 0, as it should be.
+// act(g) * u
 __device__ __forceinline__ float silu_mul(float g, float u) {
-    return __fmul_rn(__fdividef(g, __fadd_rn(1.0f, __expf(-g))), u);
+    return __fmul_rn(__fmul_rn(g, sigmoid_approx(g)), u);
 }
 __device__ __forceinline__ float gelu_mul(float g, float u) {
-    const float p = __fmul_rn(__fmul_rn(1.5957691216057308f, g), __fmaf_rn(__fmul_rn(0.044715f, g), g, 1.0f));
-    return __fmul_rn(__fdividef(g, __fadd_rn(1.0f, __expf(-p))), u);
+    return __fmul_rn(__fmul_rn(g, sigmoid_approx(gelu_exponent(g))), u);
 }
 template <int N>
 __device__ __forceinline__ void activate(const float (&g)[N], const float (&u)[N], int act, float (&h)[N]) {
@@ -87,21 +84,27 @@ __device__ __forceinline__ void activate(const float (&g)[N], const float (&u)[N
     }
 }
 
-// N consecutive columns of one row (`row`: its first element), columns below `cols` only
+// N consecutive columns of one row (`row`: its first element), columns below `cols` only.
+// align: the bytes that bases and row pitches are multiples of (32, 16 or less).
 template <int YT, int N>
-__device__ __forceinline__ void store_cols(typename OutT<YT>::T* row, int col0, int cols, bool vec, const float (&v)[N]) {
-    constexpr int PER = YT == kF32 ? 8 : 16;         // elements of a 32-byte store
+__device__ __forceinline__ void store_cols(typename OutT<YT>::T* row, int col0, int cols, int align, const float (&v)[N]) {
+    constexpr int PER = YT == kF32 ? 8 : 16;         // elements of 32 bytes
 #pragma unroll
     for (int c = 0; c < N / PER; ++c) {
         const int col = col0 + c * PER;
-        if (vec && col + PER <= cols) {
+        if (align >= 16 && col + PER <= cols) {
             uint32_t w[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 if constexpr (YT == kF32) w[i] = __float_as_uint(v[c * PER + i]);
                 else w[i] = pack2<YT>(v[c * PER + 2 * i], v[c * PER + 2 * i + 1]);
             }
-            st_v8(row + col, w);
+            if (align >= 32) {
+                st_v8(row + col, w);
+            } else {
+                st_v4(row + col, make_uint4(w[0], w[1], w[2], w[3]));
+                st_v4(row + col + PER / 2, make_uint4(w[4], w[5], w[6], w[7]));
+            }
         } else {
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
@@ -370,11 +373,11 @@ gated_mm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
 #pragma unroll
                     for (int i = 0; i < 8; ++i) accum[8 * c + i] = make_float2(h[2 * i], h[2 * i + 1]);
                 } else if (row_ok) {
-                    store_cols<YT>(static_cast<T*>(p.h) + static_cast<int64_t>(row) * p.I, col0 + 16 * c, p.I, p.vec_h, h);
+                    store_cols<YT>(static_cast<T*>(p.h) + static_cast<int64_t>(row) * p.I, col0 + 16 * c, p.I, p.align_h, h);
                     if (!FINE && p.gu) {
                         T* grow = static_cast<T*>(p.gu) + static_cast<int64_t>(row) * 2 * p.I;
-                        store_cols<YT>(grow, col0 + 16 * c, p.I, p.vec_gu, g);
-                        store_cols<YT>(grow + p.I, col0 + 16 * c, p.I, p.vec_gu, u);
+                        store_cols<YT>(grow, col0 + 16 * c, p.I, p.align_gu, g);
+                        store_cols<YT>(grow + p.I, col0 + 16 * c, p.I, p.align_gu, u);
                     }
                 }
             }
@@ -406,8 +409,11 @@ gated_mm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
                             w[i] = encode4(v, scale, p.fmt);
                         }
                         const int col = col0 + 32 * c;
-                        if (p.vec_q && col + 32 <= p.I) {
+                        if (p.align_q >= 32 && col + 32 <= p.I) {
                             st_v8(qrow + col, w);
+                        } else if (p.align_q >= 16 && col + 32 <= p.I) {
+                            st_v4(qrow + col, make_uint4(w[0], w[1], w[2], w[3]));
+                            st_v4(qrow + col + 16, make_uint4(w[4], w[5], w[6], w[7]));
                         } else {
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
@@ -490,7 +496,7 @@ gated_mm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
                     if (lane == 0) p.sinv[static_cast<int64_t>(row) * p.groups + nb] = sinv;
                     const uint32_t w = encode4(h, scale, p.fmt);
                     uint8_t* d = p.q + static_cast<int64_t>(row) * p.I + col;
-                    if (p.vec_q && col + 4 <= p.I) st_u32(d, w);
+                    if (p.align_q >= 16 && col + 4 <= p.I) st_u32(d, w);
                     else
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
@@ -677,11 +683,11 @@ gated_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
                 }
                 activate(g, u, p.act, h);
                 if (row < p.M && col0 < p.I) {
-                    store_cols<YT>(static_cast<T*>(p.h) + static_cast<int64_t>(row) * p.I, col0, p.I, p.vec_h, h);
+                    store_cols<YT>(static_cast<T*>(p.h) + static_cast<int64_t>(row) * p.I, col0, p.I, p.align_h, h);
                     if (p.gu) {
                         T* grow = static_cast<T*>(p.gu) + static_cast<int64_t>(row) * 2 * p.I;
-                        store_cols<YT>(grow, col0, p.I, p.vec_gu, g);
-                        store_cols<YT>(grow + p.I, col0, p.I, p.vec_gu, u);
+                        store_cols<YT>(grow, col0, p.I, p.align_gu, g);
+                        store_cols<YT>(grow + p.I, col0, p.I, p.align_gu, u);
                     }
                 }
             }
@@ -738,7 +744,8 @@ template <bool FINE, int OUT>
 cudaError_t launch_gated(const CUtensorMap& ma, const CUtensorMap& mg, const CUtensorMap& mu, GatedParams& p,
                          uint32_t idesc, cudaStream_t s) {
     auto kernel = gated_mm_kernel<FINE, OUT>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGatedSmemBytes);
+    static std::atomic<bool> allowed[64];
+    const cudaError_t e = allow_smem(kernel, kGatedSmemBytes, allowed);
     if (e != cudaSuccess) return e;
     static std::atomic<int> fit[4][64];
     cudaLaunchConfig_t cfg = {};
@@ -775,7 +782,8 @@ template <int YT>
 cudaError_t launch_gated_pair(const CUtensorMap& ma, const CUtensorMap& mg, const CUtensorMap& mu, const GatedParams& p,
                               uint32_t idesc, cudaStream_t s) {
     auto kernel = pair::gated_pair_kernel<YT>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, pair::kGatedSmem);
+    static std::atomic<bool> allowed[64];
+    const cudaError_t e = allow_smem(kernel, pair::kGatedSmem, allowed);
     if (e != cudaSuccess) return e;
     static std::atomic<int> fit[64];
     cudaLaunchConfig_t cfg = {};
@@ -831,10 +839,13 @@ fp8q_status launch_gated_mm(const GatedProblem& g, cudaStream_t s) {
     p.sinv = g.sinv;
     p.groups = p.tiles_n;
     const int eb = g.yt == kF32 ? 4 : 2;
-    auto rows32 = [](const void* base, int64_t pitch) { return reinterpret_cast<uintptr_t>(base) % 32 == 0 && pitch % 32 == 0; };
-    p.vec_h = rows32(g.h, I * eb);
-    p.vec_gu = rows32(g.gate_up, I * eb);
-    p.vec_q = rows32(g.q, I);
+    auto align_of = [](const void* base, int64_t pitch) {
+        const uint64_t bits = reinterpret_cast<uintptr_t>(base) | static_cast<uint64_t>(pitch);
+        return bits % 32 == 0 ? 32 : bits % 16 == 0 ? 16 : 1;
+    };
+    p.align_h = align_of(g.h, I * eb);
+    p.align_gu = align_of(g.gate_up, I * eb);
+    p.align_q = align_of(g.q, I);
     p.fmt = g.fmt;
     p.rule = g.rule;
     p.act = g.act;

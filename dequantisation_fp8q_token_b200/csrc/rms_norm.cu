@@ -589,7 +589,8 @@ fp8q_status run_bwd_vec(const BwdParams& p0, int64_t* parts, cudaStream_t s) {
     p.stages = per_cta / stage < kBwdMaxStages ? per_cta / stage : kBwdMaxStages;
     const int smem = p.stages * stage;
     auto kernel = rms_norm_bwd_vec_kernel<XT, WT, K>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<bool> allowed[64];
+    const cudaError_t e = allow_smem(kernel, kSmemPerSm, allowed);
     if (e != cudaSuccess) return cuda_status(e);
     const int64_t cap = (per_cta == kSmemPerSm ? 1LL : 2LL) * sm_count(), want = (p.m + rows - 1) / rows;
     *parts = want < cap ? want : cap;

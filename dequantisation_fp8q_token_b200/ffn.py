@@ -13,15 +13,15 @@ Allocating helpers:
 """
 from __future__ import annotations
 
+import functools
 from typing import Optional
 
 import torch
 from torch.autograd.function import once_differentiable
 
 from . import (E4M3FN, E5M2, K_MAJOR, MN_MAJOR, SCALE_IEEE, _FMT_DTYPE, _FP8_DTYPES, _check, _dev_ptr, _dtype_code,
-               _fmt_of, _need, _rule_of, _status_word, _stream, fp8q_cast_per_tensor_ex,
-               fp8q_cast_per_tensor_workspace_bytes, fp8q_scaled_mm_blockwise, fp8q_scaled_mm_ex, lib, linear_fp8,
-               per_token_cast_to_fp8)
+               _fmt_of, _need, _rule_of, _status_word, _stream, fp8q_cast_per_tensor_workspace_bytes,
+               fp8q_scaled_mm_blockwise, lib, linear_fp8, per_token_cast_to_fp8)
 
 __all__ = [
     "fp8q_rms_norm_quant", "fp8q_rms_norm_bwd", "fp8q_rms_norm_bwd_workspace_bytes",
@@ -31,6 +31,7 @@ __all__ = [
 ]
 
 ACT_SILU, ACT_GELU_TANH = 0, 1
+_CAST_WORKSPACE = functools.cache(fp8q_cast_per_tensor_workspace_bytes)      # a constant of the library
 
 
 # ---------------------------------------------------------------------------
@@ -111,24 +112,45 @@ def fp8q_rms_norm_bwd(dy: torch.Tensor, r: torch.Tensor, weight: torch.Tensor, r
         _stream(stream, dev)), "fp8q_rms_norm_bwd")
 
 
+# The autograd functions call the library directly: what they allocate themselves needs no checks, and
+# a small training step is bound by the host's time between launches.
+def _on_device(x: torch.Tensor, *others) -> int:
+    """The stream of a call on x's device; every tensor given must be on it."""
+    if not x.is_cuda:
+        raise ValueError("the input must be a CUDA tensor (libfp8q takes device pointers)")
+    for t in others:
+        if t is not None and t.device != x.device:
+            raise ValueError(f"a tensor is on {t.device}, expected {x.device}")
+    return _stream(None, x.device)
+
+
+def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
 class _RmsNorm(torch.autograd.Function):
     """rms_norm and its gradient; saves the summed rows, the weight and one rstd per row."""
 
     @staticmethod
     def forward(ctx, x, weight, residual, eps):
+        st = _on_device(x, weight, residual)
+        _like(residual, x, "residual")
         x, weight = x.contiguous(), weight.contiguous()
-        m, _ = _rows(x, weight)
+        m, n = _rows(x, weight)
         y = torch.empty_like(x)
         rstd = torch.empty((m,), dtype=torch.float32, device=x.device)
         r = None
         if residual is not None:
             residual = residual.contiguous()
             r = torch.empty_like(x)
-        fp8q_rms_norm_quant(x, weight, y=y, residual=residual, residual_out=r, rstd=rstd, eps=eps)
-        ctx.has_residual = residual is not None
+        _check(lib().fp8q_rms_norm_quant(
+            x.data_ptr(), _dtype_code(x, "x"), _ptr(residual), _ptr(r), weight.data_ptr(),
+            _dtype_code(weight, "weight"), m, n, eps, 1, E4M3FN, SCALE_IEEE, y.data_ptr(), None, None, rstd.data_ptr(),
+            st), "fp8q_rms_norm_quant")
+        ctx.has_residual = r is not None
         ctx.set_materialize_grads(False)
         ctx.save_for_backward(x if r is None else r, weight, rstd)
-        return (y, r) if ctx.has_residual else y
+        return y if r is None else (y, r)
 
     @staticmethod
     @once_differentiable
@@ -136,15 +158,21 @@ class _RmsNorm(torch.autograd.Function):
         r, weight, rstd = ctx.saved_tensors
         if dy is None:                       # only the sum was used
             return dr, None, dr if ctx.has_residual else None, None
+        st = _on_device(r, dy, dr)
         dy = dy.contiguous()
         dr = dr.contiguous() if dr is not None else None
+        m, n = _rows(r, weight)
         dx = torch.empty_like(r)
         dw = ws = None
+        nbytes = 0
         if ctx.needs_input_grad[1]:
             dw = torch.empty_like(weight)
             # a workspace of this call's own: the caching allocator orders it by stream and by graph
-            ws = torch.empty(fp8q_rms_norm_bwd_workspace_bytes(*_rows(r, weight)), dtype=torch.uint8, device=r.device)
-        fp8q_rms_norm_bwd(dy, r, weight, rstd, dx, dw, ws, dr)
+            nbytes = fp8q_rms_norm_bwd_workspace_bytes(m, n)
+            ws = torch.empty((nbytes,), dtype=torch.uint8, device=r.device)
+        _check(lib().fp8q_rms_norm_bwd(
+            dy.data_ptr(), r.data_ptr(), _dtype_code(r, "x"), weight.data_ptr(), _dtype_code(weight, "weight"),
+            rstd.data_ptr(), _ptr(dr), m, n, dx.data_ptr(), _ptr(dw), _ptr(ws), nbytes, st), "fp8q_rms_norm_bwd")
         return dx, dw, dx if ctx.has_residual else None, None
 
 
@@ -278,21 +306,18 @@ def fp8q_gated_bwd_cast(dh: torch.Tensor, gate_up: torch.Tensor, q: torch.Tensor
         workspace.numel() * workspace.element_size(), _rule_of(rule), _stream(stream, dev)), "fp8q_gated_bwd_cast")
 
 
-def _cast_workspace(device) -> torch.Tensor:
-    """A cast's workspace of the call's own: the caching allocator orders it by stream and by graph."""
-    return torch.empty(fp8q_cast_per_tensor_workspace_bytes(), dtype=torch.uint8, device=device)
-
-
-def _tensor_cast(t: torch.Tensor):
-    q = torch.empty(t.shape, dtype=torch.float8_e4m3fn, device=t.device)
-    s = torch.empty((1,), dtype=torch.float32, device=t.device)
-    fp8q_cast_per_tensor_ex(t, q, s, _cast_workspace(t.device), E4M3FN)
-    return q, s
+def _offsets(*sizes):
+    """Offsets of parts of the given byte sizes in one buffer, 256-byte aligned, and its size."""
+    at = [0]
+    for n in sizes:
+        at.append(at[-1] + (n + 255 & ~255))
+    return at
 
 
 class _GatedLinearFp8(torch.autograd.Function):
     """gated_linear_fp8: _LinearFp8's casts and products around the gated kernel and its gradient.
-    Saves the fp8 input and weight and gate and up in the input's dtype."""
+    Keeps one buffer for the backward pass: the input's and the weight's codes and scales, and gate
+    and up in the input's dtype.  Workspaces are the call's own, so that streams and graphs share none."""
 
     @staticmethod
     def forward(ctx, x, w, act):
@@ -301,38 +326,53 @@ class _GatedLinearFp8(torch.autograd.Function):
         if w.dim() != 2 or w.shape[0] % 16 or x.shape[-1] != w.shape[1] or w.shape[1] % 16:
             raise ValueError(f"weight must be [2 I, K] with 2 I and K multiples of 16 and K the input's width, got "
                              f"{tuple(w.shape)} for an input of {tuple(x.shape)}")
+        st = _on_device(x, w)
+        L, code = lib(), _dtype_code(x, "input")
         x, w = x.contiguous(), w.contiguous()
         I, K = w.shape[0] // 2, w.shape[1]
-        x2 = x.reshape(-1, K)
-        x8, sx = _tensor_cast(x2)
-        w8, sw = _tensor_cast(w)
-        h = torch.empty((x2.shape[0], I), dtype=x.dtype, device=x.device)
-        gate_up = None
-        if ctx.needs_input_grad[0] or ctx.needs_input_grad[1]:
-            gate_up = torch.empty((x2.shape[0], 2 * I), dtype=x.dtype, device=x.device)
-        fp8q_gated_mm(x8, w8[:I], w8[I:], sx, sw, sw, h, gate_up, act)
-        ctx.act, ctx.x_shape = act, x.shape
-        ctx.save_for_backward(x8, w8, sx, sw, gate_up)
-        return h.reshape(*x.shape[:-1], I)
+        T = x.numel() // K if K else 0
+        h = torch.empty((*x.shape[:-1], I), dtype=x.dtype, device=x.device)
+        keep = ctx.needs_input_grad[0] or ctx.needs_input_grad[1]
+        nws = _CAST_WORKSPACE()
+        at = _offsets(T * K, 2 * I * K, 4, 4, nws, 4 * T * I if keep else 0)
+        buf = torch.empty((at[-1],), dtype=torch.uint8, device=x.device)
+        x8, w8, sx, sw, ws, gu, _ = (buf.data_ptr() + o for o in at)
+        _check(L.fp8q_cast_per_tensor_ex(x.data_ptr(), code, T * K, E4M3FN, x8, sx, ws, nws, SCALE_IEEE, st),
+               "fp8q_cast_per_tensor")
+        _check(L.fp8q_cast_per_tensor_ex(w.data_ptr(), code, 2 * I * K, E4M3FN, w8, sw, ws, nws, SCALE_IEEE, st),
+               "fp8q_cast_per_tensor")
+        _check(L.fp8q_gated_mm(x8, E4M3FN, w8, w8 + I * K, E4M3FN, T, I, K, sx, sw, sw, act, code, h.data_ptr(),
+                               gu if keep else None, None, st), "fp8q_gated_mm")
+        ctx.sizes = act, T, I, K, at, x.shape, w.shape
+        ctx.save_for_backward(buf)
+        return h
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dh):
-        x8, w8, sx, sw, gate_up = ctx.saved_tensors
-        dh = dh.contiguous().reshape(-1, dh.shape[-1])
-        d8 = torch.empty(gate_up.shape, dtype=torch.float8_e5m2, device=dh.device)
-        sd = torch.empty((1,), dtype=torch.float32, device=dh.device)
-        fp8q_gated_bwd_cast(dh, gate_up, d8, sd, _cast_workspace(dh.device), ctx.act)
+        (buf,) = ctx.saved_tensors
+        st = _on_device(buf, dh)
+        act, T, I, K, at, x_shape, w_shape = ctx.sizes
+        x8, w8, sx, sw, _, gu, _ = (buf.data_ptr() + o for o in at)
+        L, code = lib(), _dtype_code(dh, "the gradient")
+        dh = dh.contiguous()
+        nws = _CAST_WORKSPACE()
+        to = _offsets(2 * T * I, 4, nws)
+        tmp = torch.empty((to[-1],), dtype=torch.uint8, device=buf.device)
+        d8, sd, ws, _ = (tmp.data_ptr() + o for o in to)
+        _check(L.fp8q_gated_bwd_cast(dh.data_ptr(), gu, code, T, I, act, E5M2, d8, sd, ws, nws, SCALE_IEEE, st),
+               "fp8q_gated_bwd_cast")
         dx = dw = None
         if ctx.needs_input_grad[0]:
             # dx[T, K] = d[T, 2 I] @ w[2 I, K], one product over gate's and up's columns together
-            dx = torch.empty(x8.shape, dtype=dh.dtype, device=dh.device)
-            fp8q_scaled_mm_ex(d8, w8, sd, sw, dx, a_layout=K_MAJOR, b_layout=MN_MAJOR)
-            dx = dx.reshape(ctx.x_shape)
+            dx = torch.empty(x_shape, dtype=dh.dtype, device=buf.device)
+            _check(L.fp8q_scaled_mm_ex(d8, E5M2, K_MAJOR, w8, E4M3FN, MN_MAJOR, T, K, 2 * I, sd, sw, None, code,
+                                       dx.data_ptr(), None, st), "fp8q_scaled_mm_ex")
         if ctx.needs_input_grad[1]:
-            # dw[2 I, K] = d^T[2 I, T] @ x[T, K]
-            dw = torch.empty(w8.shape, dtype=dh.dtype, device=dh.device)
-            fp8q_scaled_mm_ex(d8, x8, sd, sx, dw, a_layout=MN_MAJOR, b_layout=MN_MAJOR)
+            # dw[2 I, K] = d^T[2 I, T] @ x[T, K], any token count
+            dw = torch.empty(w_shape, dtype=dh.dtype, device=buf.device)
+            _check(L.fp8q_scaled_mm_ex(d8, E5M2, MN_MAJOR, x8, E4M3FN, MN_MAJOR, 2 * I, K, T, sd, sx, None, code,
+                                       dw.data_ptr(), None, st), "fp8q_scaled_mm_ex")
         return dx, dw, None
 
 
