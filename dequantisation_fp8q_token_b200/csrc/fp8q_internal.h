@@ -45,11 +45,11 @@ int resident_blocks_per_sm(Kernel kernel, int threads) {
 // kernel's tail (programmatic stream serialization: the kernel's own
 // pdl_begin() waits for that kernel to finish before touching memory).
 template <typename... KArgs, typename... Args>
-cudaError_t launch_kernel(void (*kernel)(KArgs...), dim3 grid, dim3 block, cudaStream_t s, Args... args) {
+cudaError_t launch_kernel_smem(void (*kernel)(KArgs...), dim3 grid, dim3 block, int smem, cudaStream_t s, Args... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
-    cfg.dynamicSmemBytes = 0;
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
 #if FP8Q_PDL
@@ -63,6 +63,10 @@ cudaError_t launch_kernel(void (*kernel)(KArgs...), dim3 grid, dim3 block, cudaS
     cfg.numAttrs = 0;
 #endif
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+template <typename... KArgs, typename... Args>
+cudaError_t launch_kernel(void (*kernel)(KArgs...), dim3 grid, dim3 block, cudaStream_t s, Args... args) {
+    return launch_kernel_smem(kernel, grid, block, 0, s, args...);
 }
 
 // `rule` is an fp8q_scale_rule: 0 one IEEE division, 1 torch's evaluation order
