@@ -17,11 +17,16 @@
 // activate and store.
 //
 // Three kernels' worth of shapes:
-//   gated_mm_kernel, no cluster   persistent, 128 x (128 + 128) tiles;
-//   gated_mm_kernel, clusters     when the tiles would fill at most half of
+//   gated_mm_kernel, persistent   128 x (128 + 128) tiles (kWide; kRagged where
+//     the output's rows are not multiples of 32 bytes);
+//   gated_mm_kernel, kCluster     when the tiles would fill at most half of
 //     the SMs (few rows, a narrow I): the CTAs of a cluster split the k axis
-//     of one tile, then each sums the parts of its share of the rows through
-//     distributed shared memory, in rank order, and finishes those rows;
+//     of one tile, each leaves its sums in its shared memory, and each then
+//     reads the parts of its share of the rows through distributed shared
+//     memory, adds them in rank order and finishes those rows;
+//   gated_mm_kernel, kDup2, kDup4 fine scales, at most 64 or 32 rows, a tile
+//     per CTA or cluster (DUP 2, 4): the A tile holds the rows DUP times over, so that
+//     every warp's TMEM lanes hold them and each folds 1 / DUP of the columns;
 //   gated_pair_kernel             per-tensor scales, many tiles: 256 rows on
 //     CTA pairs (tcgen05.mma.cta_group::2), the even CTA loading the tile's
 //     rows of Wg and the odd one its rows of Wu.
@@ -42,8 +47,17 @@ constexpr int kHalf = kHN / 2;                    // columns of h one epilogue w
 constexpr int kOutQuant = 3;                      // OUT: kF32, kF16, kBF16 or codes
 constexpr int kMaxSplit = 8;                      // CTAs of a cluster (the portable limit)
 constexpr int kPartPitch = kBN + 4;               // floats of a row of exchanged sums (16 bytes off a bank period)
-constexpr int kGatedSmemBytes = kRing * (kATileBytes + 2 * kHalfBBytes) + 1024 /* alignment */ + 256 /* barriers */;
+constexpr int kStagePitch = 17;                   // words of a row in an epilogue warp's staging area (an odd number)
+constexpr int kStageBytes = 32 * kStagePitch * 4;
+constexpr int kGatedSmemBytes = kRing * (kATileBytes + 2 * kHalfBBytes) + 1024 /* alignment */ + 256 /* barriers */ +
+                                kEpiWarps * kStageBytes;
 static_assert(BM * kPartPitch * 4 <= kRing * (kATileBytes + 2 * kHalfBBytes), "the exchange fits in the ring");
+
+// What a launch of gated_mm_kernel is compiled for.  The persistent forms have
+// every register of a fold thread in use, and code for the others would spill
+// some of them: 4096 x 18432 x 7168 to fp8 takes 1080 us, and took 1200 in a
+// build with 48 bytes of spills.
+enum { kWide, kRagged, kCluster, kDup2, kDup4 };
 
 struct GatedParams {
     int M, I, num_kb;
@@ -57,10 +71,10 @@ struct GatedParams {
     uint8_t* q;                 // [M][I] codes
     float* sinv;                // [M][ceil(I/128)]
     int groups;                 // ceil(I/128)
-    int align_h, align_gu, align_q;   // 32, 16 or 1: what bases and row pitches (and up's offset) are multiples of
+    int align_h, align_gu, align_q;   // 32, 16, 4 or 1: what bases and row pitches (and up's offset) are multiples of
     int fmt, rule;              // of the codes
     int act;
-    int stage_tx;               // bytes one stage's TMA boxes bring
+    int a_rows;                 // rows of A's TMA box
     int split;                  // CTAs that share a tile's k axis
     uint32_t* status;
     uint64_t wait_limit_ns;
@@ -118,6 +132,46 @@ __device__ __forceinline__ void store_cols(typename OutT<YT>::T* row, int col0, 
     }
 }
 
+// 16 columns of one row whose base and pitch are multiples of 32 bytes, so that a vector of its
+// columns is whole or not there
+template <int YT>
+__device__ __forceinline__ void store_cols_wide(typename OutT<YT>::T* row, int col0, int cols, const float (&v)[16]) {
+    constexpr int PER = YT == kF32 ? 8 : 16;         // elements of 32 bytes
+#pragma unroll
+    for (int c = 0; c < 16 / PER; ++c) {
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if constexpr (YT == kF32) w[i] = __float_as_uint(v[c * PER + i]);
+            else w[i] = pack2<YT>(v[c * PER + 2 * i], v[c * PER + 2 * i + 1]);
+        }
+        if (col0 + c * PER < cols) st_v8(row + col0 + c * PER, w);
+    }
+}
+// 16 columns of a warp's 32 rows where no vector may be stored: through the
+// warp's staging area, so that lanes then write neighbouring elements (half a
+// warp a row) instead of one column of 32 rows.  row0: the warp's first row.
+template <int YT>
+__device__ __forceinline__ void store_cols_staged(typename OutT<YT>::T* base, int64_t pitch, int row0, int rows, int col0,
+                                                  int cols, const float (&v)[16], float* stage) {
+    const int lane = threadIdx.x & 31;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) stage[lane * kStagePitch + i] = v[i];
+    __syncwarp();
+    const int col = col0 + (lane & 15);
+#pragma unroll 4
+    for (int r = lane >> 4; r < 32; r += 2) {
+        if (row0 + r < rows && col < cols) {
+            const float f = stage[r * kStagePitch + (lane & 15)];
+            typename OutT<YT>::T* d = base + (row0 + r) * pitch + col;
+            if constexpr (YT == kF32) *d = f;
+            else if constexpr (YT == kF16) *d = __float2half_rn(f);
+            else *d = __float2bfloat16_rn(f);
+        }
+    }
+}
+
 template <int N> __device__ __forceinline__ uint32_t absmax_of(const float (&v)[N]) {
     uint32_t a = 0u;                                 // magnitude bits: a NaN stays the maximum
 #pragma unroll
@@ -140,11 +194,21 @@ __device__ __forceinline__ uint32_t encode4(const float* v, float scale, int fmt
 // ---------------------------------------------------------------------------
 // one CTA per tile, or a cluster per tile that splits its k axis
 // ---------------------------------------------------------------------------
-template <bool FINE, int OUT>
+__device__ __forceinline__ float4 ld_cluster16(uint32_t a) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+    return v;
+}
+
+template <bool FINE, int OUT, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
 gated_mm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_g,
                 const __grid_constant__ CUtensorMap map_u, const GatedParams p, const uint32_t idesc) {
     constexpr int YT = OUT == kOutQuant ? kBF16 : OUT;
+    constexpr int DUP = MODE == kDup4 ? 4 : MODE == kDup2 ? 2 : 1;
+    constexpr bool kSingle = MODE >= kCluster;       // one tile per CTA or cluster, finished by exchange
+    constexpr int kCols = kHalf / DUP;               // columns of gate, and of up, that a thread folds
     using T = typename OutT<YT>::T;
     extern __shared__ uint8_t smem_raw[];
     __shared__ int s_abort;
@@ -153,6 +217,7 @@ gated_mm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
     uint8_t* sA = smem;
     uint8_t* sB = smem + kRing * kATileBytes;
     uint64_t* bars = reinterpret_cast<uint64_t*>(sB + kRing * 2 * kHalfBBytes);
+    float* stage_base = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(bars) + 256);
     // bars: full[kRing], empty[kRing], tfull[kAccs], tempty[kAccs], drain, amax[4]
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kRing + 2 * kAccs + 1 + 4);
     const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kRing;
@@ -192,14 +257,18 @@ gated_mm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
     pdl_begin();
 
     const int tiles = p.tiles_m * p.tiles_n;
-    const int rank = p.split > 1 ? static_cast<int>(pair::cta_rank()) : 0;
-    const int first = blockIdx.x / p.split, stride = gridDim.x / p.split;
+    const int split = kSingle ? p.split : 1;
+    const int rank = split > 1 ? static_cast<int>(pair::cta_rank()) : 0;
+    const int first = blockIdx.x / split, stride = gridDim.x / split;
     // this CTA's k-blocks
-    const int kb0 = static_cast<int>(static_cast<int64_t>(p.num_kb) * rank / p.split);
-    const int kb1 = static_cast<int>(static_cast<int64_t>(p.num_kb) * (rank + 1) / p.split);
+    const int kb0 = kSingle ? static_cast<int>(static_cast<int64_t>(p.num_kb) * rank / split) : 0;
+    const int kb1 = kSingle ? static_cast<int>(static_cast<int64_t>(p.num_kb) * (rank + 1) / split) : p.num_kb;
     uint32_t fail = 0;
-    // epilogue: this thread's row, 64 columns of gate then 64 of up, as fp32 pairs
-    float2 accum[kHalf];
+    // epilogue: this thread's row, kCols columns of gate then as many of up, as fp32 pairs
+    float2 accum[kCols];
+    // its row and first column within the tile; a warp may read TMEM lanes 32 * (warp % 4) .. + 31
+    auto row_of = [&] { return (DUP == 1 ? warp & 3 : DUP == 2 ? warp & 1 : 0) * 32 + lane; };
+    auto col_of = [&] { return ((warp - 2) >> 2) * kHalf + (DUP == 1 ? 0 : DUP == 2 ? (warp & 3) >> 1 : warp & 3) * kCols; };
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
@@ -213,8 +282,10 @@ gated_mm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
                 for (int kb = kb0; kb < kb1; ++kb) {
                     if (!mbar_wait(empty0 + 8 * stage, phase ^ 1u, abort, p.wait_limit_ns)) { fail = kTimeoutProducer; break; }
                     const uint32_t fb = full0 + 8 * stage;
-                    mbar_arrive_expect_tx(fb, static_cast<uint32_t>(p.stage_tx));
-                    tma_load_2d(smem_u32(sA + stage * kATileBytes), &map_a, kb * BK, mb * BM, fb);
+                    mbar_arrive_expect_tx(fb, static_cast<uint32_t>((DUP * p.a_rows + kBN) * BK));
+#pragma unroll
+                    for (int d = 0; d < DUP; ++d)
+                        tma_load_2d(smem_u32(sA + stage * kATileBytes + d * (kATileBytes / DUP)), &map_a, kb * BK, mb * BM, fb);
                     tma_load_2d(smem_u32(sB + stage * 2 * kHalfBBytes), &map_g, kb * BK, nb * kHN, fb);
                     tma_load_2d(smem_u32(sB + stage * 2 * kHalfBBytes + kHalfBBytes), &map_u, kb * BK, nb * kHN, fb);
                     ++issued;
@@ -264,66 +335,69 @@ gated_mm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
         }
     } else {
         // ------------------------------------------------------------ epilogue
-        const int quarter = warp & 3;                 // TMEM lanes this warp may read
-        const int half = (warp - 2) >> 2;             // which 64 columns of h
+        const int quarter = warp & 3, half = (warp - 2) >> 2;
+        const int trow = row_of(), tcol = col_of();
         const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
+        float* stage_area = stage_base + (warp - 2) * (kStageBytes / 4);
         int acc = 0;
         uint32_t acc_phase = 0, amax_phase = 0;
-        float sg = 0.0f, su = 0.0f;
+        float sg_all = 0.0f, su_all = 0.0f;
         if (!FINE) {
             const float sa = __ldg(p.sa);
-            sg = __fmul_rn(sa, __ldg(p.sg));
-            su = __fmul_rn(sa, __ldg(p.su));
+            sg_all = __fmul_rn(sa, __ldg(p.sg));
+            su_all = __fmul_rn(sa, __ldg(p.su));
         }
         for (int t = first; t < tiles && !fail; t += stride) {
             int mb, nb;
             tile_coords(t, p.tiles_m, p.tiles_n, mb, nb);
-            const int trow = quarter * 32 + lane;
             const int row = mb * BM + trow;
             const bool row_ok = row < p.M;
             const bool warp_rows_live = row - lane < p.M;
 #pragma unroll
-            for (int i = 0; i < kHalf; ++i) accum[i] = make_float2(0.0f, 0.0f);
-            if (FINE) {
-                const float* sa_row = p.sa + static_cast<int64_t>(row_ok ? row : 0) * p.ld;
-                const float* sg_row = p.sg + static_cast<int64_t>(nb) * p.ld;
-                const float* su_row = p.su + static_cast<int64_t>(nb) * p.ld;
-                float sa_next = 0.0f, sg_next = 0.0f, su_next = 0.0f;
+            for (int i = 0; i < kCols; ++i) accum[i] = make_float2(0.0f, 0.0f);
+            if constexpr (FINE) {
+                // rows past M fold with the last row's scales; nothing reads their sums
+                const float* sa_next = p.sa + static_cast<int64_t>(row_ok ? row : p.M - 1) * p.ld + kb0;
+                const float* sg_next = p.sg + static_cast<int64_t>(nb) * p.ld + kb0;
+                const float* su_next = p.su + static_cast<int64_t>(nb) * p.ld + kb0;
+                float sa = 0.0f, sg = 0.0f, su = 0.0f;
                 if (kb0 < kb1) {
-                    sa_next = row_ok ? __ldg(sa_row + kb0) : 0.0f;
-                    sg_next = __ldg(sg_row + kb0);
-                    su_next = __ldg(su_row + kb0);
+                    sa = __ldg(sa_next);
+                    sg = __ldg(sg_next);
+                    su = __ldg(su_next);
                 }
                 for (int kb = kb0; kb < kb1; ++kb) {
-                    const float g1 = __fmul_rn(sa_next, sg_next), u1 = __fmul_rn(sa_next, su_next);
+                    const float g1 = __fmul_rn(sa, sg), u1 = __fmul_rn(sa, su);
                     if (kb + 1 < kb1) {
-                        sa_next = row_ok ? __ldg(sa_row + kb + 1) : 0.0f;
-                        sg_next = __ldg(sg_row + kb + 1);
-                        su_next = __ldg(su_row + kb + 1);
+                        sa = __ldg(++sa_next);
+                        sg = __ldg(++sg_next);
+                        su = __ldg(++su_next);
                     }
                     const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(tfull0 + 8 * acc, acc_phase, abort, p.wait_limit_ns));
                     if (!ok) { fail = kTimeoutEpilogue; break; }
                     tc_fence_after();
                     if (warp_rows_live) {
-                        // four chunks of 16 columns of gate, then four of up; the load of the
+                        // chunks of 16 columns of gate, then as many of up; the load of the
                         // next chunk is in flight while one is folded in
-                        const uint32_t addr = tmem_base + lane_addr + static_cast<uint32_t>(acc * kBN + half * kHalf);
+                        constexpr int kChunks = kCols / 16;
+                        const uint32_t addr = tmem_base + lane_addr + static_cast<uint32_t>(acc * kBN + tcol);
                         const float2 g2 = make_float2(g1, g1), u2 = make_float2(u1, u1);
                         uint32_t r0[16], r1[16];
                         tmem_ld16_async(addr, r0);
                         tmem_wait16(r0);
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) {
+                        for (int c = 0; c < 2 * kChunks; ++c) {
                             uint32_t (&cur)[16] = (c & 1) ? r1 : r0;
                             uint32_t (&nxt)[16] = (c & 1) ? r0 : r1;
                             const int n = c + 1;
-                            if (n < 8) tmem_ld16_async(addr + static_cast<uint32_t>(n < 4 ? 16 * n : kHN + 16 * (n - 4)), nxt);
+                            if (n < 2 * kChunks)
+                                tmem_ld16_async(addr + static_cast<uint32_t>(n < kChunks ? 16 * n : kHN + 16 * (n - kChunks)), nxt);
 #pragma unroll
                             for (int i = 0; i < 8; ++i)
                                 accum[c * 8 + i] = __ffma2_rn(make_float2(__uint_as_float(cur[2 * i]),
                                                                           __uint_as_float(cur[2 * i + 1])),
-                                                              c < 4 ? g2 : u2, accum[c * 8 + i]);
-                            if (n < 8) tmem_wait16(nxt);
+                                                              c < kChunks ? g2 : u2, accum[c * 8 + i]);
+                            if (n < 2 * kChunks) tmem_wait16(nxt);
                         }
                     }
                     tc_fence_before();
@@ -337,13 +411,13 @@ gated_mm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
                 if (!ok) { fail = kTimeoutEpilogue; break; }
                 tc_fence_after();
                 if (warp_rows_live) {
-                    const uint32_t addr = tmem_base + lane_addr + static_cast<uint32_t>(acc * kBN + half * kHalf);
+                    const uint32_t addr = tmem_base + lane_addr + static_cast<uint32_t>(acc * kBN + tcol);
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         uint32_t r[32];
                         tmem_ld32_async(addr + static_cast<uint32_t>(c < 2 ? 32 * c : kHN + 32 * (c - 2)), r);
                         tmem_wait32(r);
-                        const float s = c < 2 ? sg : su;
+                        const float s = c < 2 ? sg_all : su_all;
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
                             accum[c * 16 + i] = make_float2(__fmul_rn(__uint_as_float(r[2 * i]), s),
@@ -355,8 +429,9 @@ gated_mm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
                 if (lane == 0) mbar_arrive(tempty0 + 8 * acc);
                 if (++acc == kAccs) { acc = 0; acc_phase ^= 1u; }
             }
-            if (p.split > 1 || !warp_rows_live) continue;      // a cluster finishes its one tile below
-            const int col0 = nb * kHN + half * kHalf;
+            if (kSingle || !warp_rows_live) continue;      // a single tile is finished below
+            if constexpr (!kSingle) {
+            const int col0 = nb * kHN + tcol;
             // 16 columns at a time, the activated values over gate's registers
 #pragma unroll
             for (int c = 0; c < kHalf / 16; ++c) {
@@ -372,12 +447,21 @@ gated_mm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
                 if constexpr (OUT == kOutQuant) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) accum[8 * c + i] = make_float2(h[2 * i], h[2 * i + 1]);
-                } else if (row_ok) {
-                    store_cols<YT>(static_cast<T*>(p.h) + static_cast<int64_t>(row) * p.I, col0 + 16 * c, p.I, p.align_h, h);
+                } else {
+                    auto put = [&](void* out, int64_t pitch, int align, const float (&v)[16]) {
+                        T* base = static_cast<T*>(out);
+                        if constexpr (MODE == kWide) {
+                            if (row_ok) store_cols_wide<YT>(base + row * pitch, col0 + 16 * c, p.I, v);
+                        } else if (align >= 16) {
+                            if (row_ok) store_cols<YT>(base + row * pitch, col0 + 16 * c, p.I, align, v);
+                        } else {
+                            store_cols_staged<YT>(base, pitch, row - lane, p.M, col0 + 16 * c, p.I, v, stage_area);
+                        }
+                    };
+                    put(p.h, p.I, p.align_h, h);
                     if (!FINE && p.gu) {
-                        T* grow = static_cast<T*>(p.gu) + static_cast<int64_t>(row) * 2 * p.I;
-                        store_cols<YT>(grow, col0 + 16 * c, p.I, p.align_gu, g);
-                        store_cols<YT>(grow + p.I, col0 + 16 * c, p.I, p.align_gu, u);
+                        put(p.gu, 2 * static_cast<int64_t>(p.I), p.align_gu, g);
+                        put(static_cast<T*>(p.gu) + p.I, 2 * static_cast<int64_t>(p.I), p.align_gu, u);
                     }
                 }
             }
@@ -396,84 +480,102 @@ gated_mm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
                 float scale, sinv;
                 group_scales(max(mine, s_amax[amax_phase][half ^ 1][trow]), p.fmt, p.rule, scale, sinv);
                 amax_phase ^= 1u;
-                if (row_ok) {
-                    if (half == 0) p.sinv[static_cast<int64_t>(row) * p.groups + nb] = sinv;
-                    uint8_t* qrow = p.q + static_cast<int64_t>(row) * p.I;
+                if (row_ok && half == 0) p.sinv[static_cast<int64_t>(row) * p.groups + nb] = sinv;
+                auto word = [&](int i) {             // codes 4 i .. 4 i + 3
+                    const float v[4] = {accum[2 * i].x, accum[2 * i].y, accum[2 * i + 1].x, accum[2 * i + 1].y};
+                    return encode4(v, scale, p.fmt);
+                };
+                if constexpr (MODE == kWide) {
+                    uint8_t* qrow = p.q + static_cast<int64_t>(row) * p.I + col0;
 #pragma unroll
                     for (int c = 0; c < kHalf / 32; ++c) {
                         uint32_t w[8];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float v[4] = {accum[16 * c + 2 * i].x, accum[16 * c + 2 * i].y,
-                                                accum[16 * c + 2 * i + 1].x, accum[16 * c + 2 * i + 1].y};
-                            w[i] = encode4(v, scale, p.fmt);
-                        }
-                        const int col = col0 + 32 * c;
-                        if (p.align_q >= 32 && col + 32 <= p.I) {
-                            st_v8(qrow + col, w);
-                        } else if (p.align_q >= 16 && col + 32 <= p.I) {
-                            st_v4(qrow + col, make_uint4(w[0], w[1], w[2], w[3]));
-                            st_v4(qrow + col + 16, make_uint4(w[4], w[5], w[6], w[7]));
-                        } else {
+                        for (int i = 0; i < 8; ++i) w[i] = word(8 * c + i);
+                        if (row_ok && col0 + 32 * c < p.I) st_v8(qrow + 32 * c, w);
+                    }
+                } else {
+                    // as store_cols_staged: half a warp writes a row's 64 codes, as words where they
+                    // are aligned, else 16 bytes at a time
+                    uint32_t* area = reinterpret_cast<uint32_t*>(stage_area);
+                    __syncwarp();
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (col + i < p.I) qrow[col + i] = static_cast<uint8_t>(w[i / 4] >> (8 * (i % 4)));
+                    for (int i = 0; i < kHalf / 4; ++i)
+                        asm volatile("st.shared.b32 [%0], %1;" :: "r"(smem_u32(area + lane * kStagePitch + i)), "r"(word(i)) : "memory");
+                    __syncwarp();
+                    const int l = lane & 15;
+                    for (int r = lane >> 4; r < 32 && row - lane + r < p.M; r += 2) {
+                        uint8_t* qrow = p.q + static_cast<int64_t>(row - lane + r) * p.I + col0;
+                        if (p.align_q >= 4) {
+                            if (col0 + 4 * l < p.I) st_u32(qrow + 4 * l, area[r * kStagePitch + l]);
+                        } else {
+                            const uint8_t* codes = reinterpret_cast<const uint8_t*>(area + r * kStagePitch);
+#pragma unroll
+                            for (int c = l; c < kHalf; c += 16)
+                                if (col0 + c < p.I) qrow[c] = codes[c];
                         }
                     }
                 }
+            }
             }
         }
         if (fail && lane == 0) *abort = 1;
     }
 
-    if (p.split > 1) {
-        // The cluster's one tile: rank r finishes rows [r * share, (r + 1) * share) of the live
-        // ones.  Every CTA's copies and MMAs are done (drained above), so once all have arrived
-        // the rings hold nothing: each thread writes its row's sums into the owner's ring.
+    if constexpr (kSingle) {
+        // The one tile of this CTA or cluster: rank r finishes rows [r * share, (r + 1) * share)
+        // of the live ones.  This CTA's copies and MMAs are done (drained above), so past the
+        // barrier its ring holds nothing and takes its sums, row by row.
         int mb, nb;
         tile_coords(first, p.tiles_m, p.tiles_n, mb, nb);
         const int live = min(BM, p.M - mb * BM);
-        const int share = (live + p.split - 1) / p.split;
-        __syncwarp();
-        pair::cluster_sync();
-        if (warp >= 2) {
-            const int trow = (warp & 3) * 32 + lane, half = (warp - 2) >> 2;
-            if (trow < live) {
-                const int owner = trow / share;
-                // [source rank][row of the owner's share][gate 0..127, up 0..127]
-                const uint32_t local = smem_u32(smem) +
-                    4u * static_cast<uint32_t>((rank * share + trow - owner * share) * kPartPitch + half * kHalf);
-                uint32_t dst;
-                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(dst) : "r"(local), "r"(owner));
+        const int share = (live + split - 1) / split;
+        __syncthreads();
+        const int trow = row_of(), tcol = col_of();
+        if (warp >= 2 && trow < live) {
+            float* dst = reinterpret_cast<float*>(smem) + trow * kPartPitch + tcol;
 #pragma unroll
-                for (int i = 0; i < kHalf / 2; ++i) {
-                    const uint32_t at = dst + (i < kHalf / 4 ? 16u * i : 4u * kHN + 16u * (i - kHalf / 4));
-                    asm volatile("st.shared::cluster.v4.f32 [%0], {%1,%2,%3,%4};"
-                                 :: "r"(at), "f"(accum[2 * i].x), "f"(accum[2 * i].y), "f"(accum[2 * i + 1].x),
-                                    "f"(accum[2 * i + 1].y) : "memory");
-                }
-            }
+            for (int i = 0; i < kCols / 2; ++i)
+                *reinterpret_cast<float4*>(dst + (i < kCols / 4 ? 4 * i : kHN + 4 * (i - kCols / 4))) =
+                    make_float4(accum[2 * i].x, accum[2 * i].y, accum[2 * i + 1].x, accum[2 * i + 1].y);
         }
         __syncwarp();
-        pair::cluster_sync();
+        if (split > 1) pair::cluster_sync();
+        else __syncthreads();
         if (warp >= 2) {
-            const float* parts = reinterpret_cast<const float*>(smem);
             for (int r = warp - 2; r < share && rank * share + r < live; r += kEpiWarps) {
                 const int row = mb * BM + rank * share + r;
                 // lane l: columns 4 l .. 4 l + 3, the ranks' sums added in rank order
+                const uint32_t mine = smem_u32(smem) + 4u * static_cast<uint32_t>((rank * share + r) * kPartPitch + 4 * lane);
+                float4 a[kMaxSplit], b[kMaxSplit];
+#pragma unroll
+                for (int s = 0; s < kMaxSplit; ++s) {
+                    if (s < split) {
+                        uint32_t src = mine;
+                        if (split > 1) asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(src) : "r"(mine), "r"(s));
+                        a[s] = ld_cluster16(src);
+                        b[s] = ld_cluster16(src + 4u * kHN);
+                    }
+                }
                 float g[4] = {0.0f, 0.0f, 0.0f, 0.0f}, u[4] = {0.0f, 0.0f, 0.0f, 0.0f}, h[4];
-                for (int s = 0; s < p.split; ++s) {
-                    const float* src = parts + static_cast<int64_t>(s * share + r) * kPartPitch;
-                    const float4 a = *reinterpret_cast<const float4*>(src + 4 * lane);
-                    const float4 b = *reinterpret_cast<const float4*>(src + kHN + 4 * lane);
-                    g[0] += a.x; g[1] += a.y; g[2] += a.z; g[3] += a.w;
-                    u[0] += b.x; u[1] += b.y; u[2] += b.z; u[3] += b.w;
+#pragma unroll
+                for (int s = 0; s < kMaxSplit; ++s) {
+                    if (s < split) {
+                        g[0] += a[s].x; g[1] += a[s].y; g[2] += a[s].z; g[3] += a[s].w;
+                        u[0] += b[s].x; u[1] += b[s].y; u[2] += b[s].z; u[3] += b[s].w;
+                    }
                 }
                 activate(g, u, p.act, h);
                 const int col = nb * kHN + 4 * lane;
                 if constexpr (OUT != kOutQuant) {
-                    auto put = [&](void* base, int64_t at, const float (&v)[4]) {
+                    auto put = [&](void* base, int64_t at, int align, const float (&v)[4]) {
                         T* d = static_cast<T*>(base) + at;
+                        if (align >= 16 && col + 4 <= p.I) {
+                            if constexpr (YT == kF32) st_v4(d, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]),
+                                                                          __float_as_uint(v[2]), __float_as_uint(v[3])));
+                            else st_v2(d, make_uint2(pack2<YT>(v[0], v[1]), pack2<YT>(v[2], v[3])));
+                            return;
+                        }
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             if (col + i >= p.I) break;
@@ -482,10 +584,10 @@ gated_mm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
                             else d[i] = __float2bfloat16_rn(v[i]);
                         }
                     };
-                    put(p.h, static_cast<int64_t>(row) * p.I + col, h);
+                    put(p.h, static_cast<int64_t>(row) * p.I + col, p.align_h, h);
                     if (!FINE && p.gu) {
-                        put(p.gu, static_cast<int64_t>(row) * 2 * p.I + col, g);
-                        put(p.gu, static_cast<int64_t>(row) * 2 * p.I + p.I + col, u);
+                        put(p.gu, static_cast<int64_t>(row) * 2 * p.I + col, p.align_gu, g);
+                        put(p.gu, static_cast<int64_t>(row) * 2 * p.I + p.I + col, p.align_gu, u);
                     }
                 } else {
                     uint32_t a = absmax_of(h);
@@ -496,7 +598,7 @@ gated_mm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
                     if (lane == 0) p.sinv[static_cast<int64_t>(row) * p.groups + nb] = sinv;
                     const uint32_t w = encode4(h, scale, p.fmt);
                     uint8_t* d = p.q + static_cast<int64_t>(row) * p.I + col;
-                    if (p.align_q >= 16 && col + 4 <= p.I) st_u32(d, w);
+                    if (p.align_q >= 4 && col + 4 <= p.I) st_u32(d, w);
                     else
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
@@ -508,6 +610,10 @@ gated_mm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
 
     if (fail && p.status && lane == 0) atomicOr(p.status, fail);
     tc_fence_before();
+    if (kSingle && split > 1) {                      // no CTA leaves while another may still read its sums
+        __syncwarp();
+        pair::cluster_sync();
+    }
     __syncthreads();
     tc_fence_after();
     if (warp == 1) {
@@ -740,14 +846,13 @@ int clusters_that_fit(Kernel kernel, cudaLaunchConfig_t cfg, int size, std::atom
     return fit;
 }
 
-template <bool FINE, int OUT>
-cudaError_t launch_gated(const CUtensorMap& ma, const CUtensorMap& mg, const CUtensorMap& mu, GatedParams& p,
-                         uint32_t idesc, cudaStream_t s) {
-    auto kernel = gated_mm_kernel<FINE, OUT>;
+template <bool FINE, int OUT, int MODE>
+cudaError_t launch_gated_mode(const CUtensorMap& ma, const CUtensorMap& mg, const CUtensorMap& mu, GatedParams& p,
+                              uint32_t idesc, cudaStream_t s) {
+    auto kernel = gated_mm_kernel<FINE, OUT, MODE>;
     static std::atomic<bool> allowed[64];
     const cudaError_t e = allow_smem(kernel, kGatedSmemBytes, allowed);
     if (e != cudaSuccess) return e;
-    static std::atomic<int> fit[4][64];
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kGatedSmemBytes;
@@ -759,23 +864,73 @@ cudaError_t launch_gated(const CUtensorMap& ma, const CUtensorMap& mg, const CUt
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
+    attr[1].val.clusterDim.x = p.split;
+    cfg.numAttrs = p.split > 1 ? 2 : 1;
     const int tiles = p.tiles_m * p.tiles_n;
-    // Split the k axis over as many CTAs as leave every tile its own cluster, at
-    // least two k-blocks each: a tile whose k axis one SM walks alone streams its
-    // weights at that SM's rate while the others idle.
-    p.split = 1;
-    cfg.numAttrs = 2;
-    for (int c = kMaxSplit, i = 3; c > 1; c /= 2, --i) {
-        if (p.num_kb < 2 * c || static_cast<int64_t>(tiles) * c > sm_count()) continue;
-        attr[1].val.clusterDim.x = c;
-        if (tiles > clusters_that_fit(kernel, cfg, c, fit[i])) continue;
-        p.split = c;
-        break;
-    }
-    if (p.split == 1) cfg.numAttrs = 1;
     const int ctas = p.split > 1 ? tiles * p.split : (tiles < sm_count() ? tiles : sm_count());
     cfg.gridDim = dim3(static_cast<unsigned>(ctas));
     return cudaLaunchKernelEx(&cfg, kernel, ma, mg, mu, p, idesc);
+}
+
+// clusters of `size` CTAs of the kernel's shape that fit on the device at once
+int split_fit(int size) {
+    static std::atomic<int> fit[kMaxSplit + 1][64];
+    auto kernel = gated_mm_kernel<true, kOutQuant, kCluster>;
+    static std::atomic<bool> allowed[64];
+    if (allow_smem(kernel, kGatedSmemBytes, allowed) != cudaSuccess) return 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kGatedSmemBytes;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = size;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return clusters_that_fit(kernel, cfg, size, fit[size]);
+}
+
+// Split the k axis over the CTAs of a cluster where that is estimated to be faster: a tile
+// whose k axis one SM walks alone streams its weights at that SM's rate while others idle.
+// In ns, from runs of 512 to 2048 columns: a k-block takes 480 (fine scales), 380 (fine
+// scales, DUP) or 330; a cluster's barriers take 1000 and its exchange 37 for each row that a
+// CTA receives parts of (14 bytes a clock through distributed shared memory); an undivided
+// tile's own epilogue takes 1200, what finishing a DUP tile takes is the same either way.
+// 128 x 2048 x 2048: 14.1 us undivided, 11.6 on 4 CTAs; 128 x 512 x 1024: 8.8 and 9.1;
+// 1 x 2048 x 7168: 25.3 undivided, 10.5 on 6.
+int choose_split(const GatedParams& p, int64_t per_kb, bool dup) {
+    const int tiles = p.tiles_m * p.tiles_n, rows = p.M < BM ? p.M : BM;
+    int split = 1;
+    int64_t best = per_kb * p.num_kb + (dup ? 0 : 1200);
+    for (int c = 2; c <= kMaxSplit && c <= p.num_kb && static_cast<int64_t>(tiles) * c <= sm_count(); ++c) {
+        const int64_t cost = per_kb * ((p.num_kb + c - 1) / c) + 1000 + 37LL * rows * (c - 1) / c;
+        if (cost >= best || tiles > split_fit(c)) continue;
+        best = cost;
+        split = c;
+    }
+    return split;
+}
+
+template <bool FINE, int OUT>
+cudaError_t launch_gated(const CUtensorMap& ma, const CUtensorMap& mg, const CUtensorMap& mu, GatedParams& p,
+                         uint32_t idesc, cudaStream_t s) {
+    if constexpr (FINE) {
+        // A fold's time is the latency of its TMEM loads: few rows share them out among all
+        // warps.  Copying A twice only pays where a cluster shares a tile (64 x 2048 x 7168:
+        // 13.5 against 14.0 us; 64 x 18432 x 7168, a tile per SM: 50.2 against 48.6).
+        const bool dup4 = p.M <= 32 && p.tiles_n <= sm_count();
+        if (dup4 || (p.M <= 64 && 2 * p.tiles_n <= sm_count())) {
+            p.split = choose_split(p, 380, true);
+            return dup4 ? launch_gated_mode<FINE, OUT, kDup4>(ma, mg, mu, p, idesc, s)
+                        : launch_gated_mode<FINE, OUT, kDup2>(ma, mg, mu, p, idesc, s);
+        }
+    }
+    p.split = choose_split(p, FINE ? 480 : 330, false);
+    if (p.split > 1) return launch_gated_mode<FINE, OUT, kCluster>(ma, mg, mu, p, idesc, s);
+    const bool wide = OUT == kOutQuant ? p.align_q >= 32 : p.align_h >= 32 && (!p.gu || p.align_gu >= 32);
+    return wide ? launch_gated_mode<FINE, OUT, kWide>(ma, mg, mu, p, idesc, s)
+                : launch_gated_mode<FINE, OUT, kRagged>(ma, mg, mu, p, idesc, s);
 }
 
 template <int YT>
@@ -841,7 +996,7 @@ fp8q_status launch_gated_mm(const GatedProblem& g, cudaStream_t s) {
     const int eb = g.yt == kF32 ? 4 : 2;
     auto align_of = [](const void* base, int64_t pitch) {
         const uint64_t bits = reinterpret_cast<uintptr_t>(base) | static_cast<uint64_t>(pitch);
-        return bits % 32 == 0 ? 32 : bits % 16 == 0 ? 16 : 1;
+        return bits % 32 == 0 ? 32 : bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 1;
     };
     p.align_h = align_of(g.h, I * eb);
     p.align_gu = align_of(g.gate_up, I * eb);
@@ -849,7 +1004,7 @@ fp8q_status launch_gated_mm(const GatedProblem& g, cudaStream_t s) {
     p.fmt = g.fmt;
     p.rule = g.rule;
     p.act = g.act;
-    p.stage_tx = (a_rows + kBN) * BK;
+    p.a_rows = a_rows;
     p.status = g.status;
     p.wait_limit_ns = kWaitLimitNs;
     cudaError_t e;

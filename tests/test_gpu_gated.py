@@ -133,6 +133,29 @@ def check_tensor(fp8q, M, I, K, yt, act="silu", fa=E4, fb=E4, with_gu=True, offs
     assert torch.equal(again, out.t)
 
 
+# the same at the borders between the kernel's forms: at most 32 and 64 rows (all rows in every
+# warp's TMEM lanes) with a cluster for a tile and with a tile for each CTA, and persistent tiles
+# whose rows are no multiples of 32 bytes (words, bytes), of 16 and of an element
+@pytest.mark.parametrize("M,I,K", [(16, 2048, 1024), (17, 2048, 1024), (32, 18000, 256), (33, 9000, 256), (64, 1536, 640),
+                                   (64, 18432, 128), (65, 9500, 128), (3, 18944, 128), (2, 19000, 128), (30, 19072, 256),
+                                   (300, 8972, 256), (300, 9001, 128), (300, 8976, 128), (140, 19001, 48)])
+def test_blockwise_forms(fp8q, M, I, K):
+    check_quant(fp8q, M, I, K)
+    for yt in (BF16, F32):
+        ops = fine_operands(M, I, K)
+        out = Guarded(M * I, yt)
+        fp8q.fp8q_gated_mm_blockwise(*ops, out.t)
+        out.check()
+        _, _, h, _, _, e = fine_reference(*ops, "silu")
+        assert ((out.t.view(M, I).double() - h).abs() <= e + h.abs() * P.half_step(yt) + P.tiny(yt)).all()
+
+
+@pytest.mark.parametrize("yt", [BF16, F16, F32])
+@pytest.mark.parametrize("M,I,K", [(250, 9001, 128), (200, 9501, 64), (250, 9004, 128), (100, 600, 1600), (128, 2048, 2048)])
+def test_per_tensor_forms(fp8q, yt, M, I, K):
+    check_tensor(fp8q, M, I, K, yt)
+
+
 # one CTA a tile, clusters, and (from 67 tiles of 256 rows) CTA pairs
 @pytest.mark.parametrize("yt", [BF16, F16, F32])
 @pytest.mark.parametrize("M,I,K", [(1, 128, 128), (300, 384, 1024), (64, 2048, 2048), (257, 1001, 256), (512, 4352, 256),
