@@ -1,10 +1,13 @@
-"""Build libfp8q.so in-tree with nvcc for sm_100a (B200).
+"""Build libfp8q.so in-tree with nvcc for sm_100a (B200), and the binding's native part.
 
     python -m dequantisation_fp8q_token_b200.build [--force] [--verbose]
 
 Each csrc/*.cu compiles to an object in _build/ (in parallel), then nvcc links
 them into dequantisation_fp8q_token_b200/libfp8q.so with the CUDA runtime
 linked statically, so the library needs only the driver at run time.
+csrc/torch_ops.cpp (marshalling and autograd functions over the C ABI, no
+device code) compiles with g++ against the installed torch into _fp8q_torch.so
+beside it.
 Flags keep IEEE semantics: no fast-math, precise division, denormals kept.
 """
 from __future__ import annotations
@@ -22,6 +25,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build", "libfp8q")
 LIB = os.path.join(PKG, "libfp8q.so")
+TORCH_SRC = os.path.join(CSRC, "torch_ops.cpp")
+TORCH_EXT = os.path.join(PKG, "_fp8q_torch.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
@@ -53,7 +58,50 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in sources() + _deps() + [__file__])
 
 
+def torch_ext_up_to_date() -> bool:
+    if not os.path.exists(TORCH_EXT):
+        return False
+    t = os.path.getmtime(TORCH_EXT)
+    return all(os.path.getmtime(p) <= t for p in (TORCH_SRC, os.path.join(INCLUDE, "fp8q.h"), __file__))
+
+
+def build_torch_ext(force: bool = False, verbose: bool = False) -> str:
+    """_fp8q_torch.so, against libfp8q.so (found beside it at run time) and the installed torch."""
+    if not force and torch_ext_up_to_date():
+        return TORCH_EXT
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    cxx = shutil.which("g++") or "g++"
+    tmp = TORCH_EXT + ".tmp.%d" % os.getpid()
+    cuda_include = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-DTORCH_EXTENSION_NAME=_fp8q_torch",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch.compiled_with_cxx11_abi(), "-I", INCLUDE]
+    for d in [*cpp_extension.include_paths(), cuda_include, sysconfig.get_paths()["include"]]:
+        cmd += ["-isystem", d]
+    cmd += [TORCH_SRC, "-o", tmp]
+    for d in cpp_extension.library_paths():
+        cmd += ["-L", d]
+    cmd += ["-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda", "-ltorch_python", "-L", PKG, "-l:libfp8q.so",
+            "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cxx} failed on {TORCH_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, TORCH_EXT)
+    return TORCH_EXT
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
+    """libfp8q.so and _fp8q_torch.so, whichever is stale; the path of the former."""
+    lib = build_lib(force, verbose, extra_flags)
+    build_torch_ext(force, verbose)
+    return lib
+
+
+def build_lib(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     if not force and up_to_date():
         return LIB
     os.makedirs(BUILD, exist_ok=True)

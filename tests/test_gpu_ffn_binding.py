@@ -1,0 +1,178 @@
+"""The native part of the norm and feed-forward binding on a GPU: refusals and status errors, streams,
+empty inputs, what the autograd functions leave behind, and training steps inside CUDA graphs."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+BF16 = torch.bfloat16
+
+
+def rand(*shape, seed=0, dt=BF16):
+    g = torch.Generator(device="cuda").manual_seed(seed + sum(shape))
+    return torch.randn(shape, generator=g, device="cuda").to(dt)
+
+
+def fine(M, I, K):
+    a, wg, wu = (rand(r, K, seed=i).to(torch.float8_e4m3fn) for i, r in enumerate((M, I, I)))
+    kb, ib = -(-K // 128), -(-I // 128)
+    return a, torch.ones(M, kb, device="cuda"), wg, torch.ones(ib, kb, device="cuda"), wu, torch.ones(ib, kb, device="cuda")
+
+
+def test_status_errors_and_refusals(fp8q):
+    x, w = rand(4, 256), rand(256)
+    q, s = torch.zeros(4, 256, dtype=torch.uint8, device="cuda"), torch.zeros(4, 2, device="cuda")
+    for kw, status in (({"eps": -1.0}, 4), ({"group": 0}, 4), ({"group": 100}, 4), ({"fmt": 7}, 3), ({"rule": 5}, 10),
+                       ({"group": 1 << 40}, 4)):
+        with pytest.raises(fp8q.Fp8qError) as e:
+            fp8q.fp8q_rms_norm_quant(x, w, q=q, scale_inv=s, **kw)
+        assert e.value.status == status and "fp8q_rms_norm_quant" in str(e.value)
+    with pytest.raises(fp8q.Fp8qError):
+        fp8q.rms_norm(x, w, eps=-1.0)
+    with pytest.raises(fp8q.Fp8qError):
+        fp8q.rms_norm(x, w.half())                                           # fp16 weight for bf16 rows
+    ops = fine(4, 64, 256)
+    h, hs = torch.zeros(4, 64, dtype=torch.uint8, device="cuda"), torch.zeros(4, 1, device="cuda")
+    for kw, status in (({"act": 5}, 4), ({"fmt": 9}, 3), ({"fa": 9}, 3), ({"rule": 4}, 10)):
+        with pytest.raises(fp8q.Fp8qError) as e:
+            fp8q.fp8q_gated_mm_blockwise_quant(*ops, h, hs, **kw)
+        assert e.value.status == status
+    with pytest.raises(fp8q.Fp8qError) as e:
+        fp8q.gated_linear_fp8(x, rand(64, 256), act=3)
+    assert e.value.status == 4
+    for call in (lambda: fp8q.fp8q_rms_norm_quant(x, w.cpu(), q=q, scale_inv=s),
+                 lambda: fp8q.fp8q_rms_norm_quant(x, w, q=q.cpu(), scale_inv=s),
+                 lambda: fp8q.fp8q_rms_norm_quant(x.t().contiguous().t(), w, q=q, scale_inv=s),      # not contiguous
+                 lambda: fp8q.rms_norm(x, w.cpu()), lambda: fp8q.rms_norm(x, w, residual=x.cpu()),
+                 lambda: fp8q.rms_norm(x, w, residual=x[:2]),
+                 lambda: fp8q.gated_linear_fp8(x, rand(64, 256).cpu()),
+                 lambda: fp8q.fp8q_gated_mm_blockwise_quant(*ops[:5], ops[5].cpu(), h, hs)):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: fp8q.fp8q_rms_norm_quant(x.double(), w, q=q, scale_inv=s), lambda: fp8q.rms_norm(x.double(), w),
+                 lambda: fp8q.fp8q_gated_mm_blockwise_quant(*ops, h, hs, status=torch.zeros(1, device="cuda")),
+                 lambda: fp8q.fp8q_rms_norm_quant(x, w, q=x, scale_inv=s)):
+        with pytest.raises(TypeError):
+            call()
+
+
+def test_streams_given_as_objects_and_handles(fp8q):
+    x, w = rand(64, 1024), rand(1024)
+    want_q, want_s = fp8q.rms_norm_cast_to_fp8(x, w)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream, None):
+        q, s = torch.zeros(64, 1024, dtype=torch.uint8, device="cuda"), torch.zeros(64, 8, device="cuda")
+        torch.cuda.synchronize()
+        fp8q.fp8q_rms_norm_quant(x, w, q=q, scale_inv=s, stream=stream)
+        (side if stream is not None else torch.cuda.current_stream()).synchronize()
+        assert torch.equal(q, want_q.view(torch.uint8)) and torch.equal(s, want_s)
+    ops = fine(9, 256, 512)
+    h, hs = torch.zeros(9, 256, dtype=torch.uint8, device="cuda"), torch.zeros(9, 2, device="cuda")
+    fp8q.fp8q_gated_mm_blockwise_quant(*ops, h, hs)
+    h2, hs2 = torch.zeros_like(h), torch.zeros_like(hs)
+    torch.cuda.synchronize()
+    fp8q.fp8q_gated_mm_blockwise_quant(*ops, h2, hs2, stream=side)
+    side.synchronize()
+    assert torch.equal(h, h2) and torch.equal(hs, hs2)
+
+
+def test_empty_inputs(fp8q):
+    w = rand(256).requires_grad_(True)
+    x = rand(0, 256).requires_grad_(True)
+    y, r = fp8q.rms_norm(x, w, residual=x.detach())
+    assert y.shape == r.shape == (0, 256)
+    dx, dw = torch.autograd.grad((y, r), (x, w), (y.detach(), r.detach()))
+    assert dx.shape == (0, 256) and (dw == 0).all()                          # no rows: zeros
+    wide = rand(64, 256, seed=3).requires_grad_(True)
+    h = fp8q.gated_linear_fp8(x, wide)
+    assert h.shape == (0, 32)
+    dx, dw = torch.autograd.grad(h, (x, wide), h.detach())
+    assert dx.shape == (0, 256) and dw.shape == (64, 256) and (dw == 0).all()
+
+
+def test_gradients_of_leaves_are_their_own(fp8q):
+    """x's and the residual's gradients are equal, and neither changes with the other; a second
+    backward pass adds to both."""
+    x, r, w = rand(8, 128), rand(8, 128, seed=1), rand(128)
+    for t in (x, r, w):
+        t.requires_grad_(True)
+    y, s = fp8q.rms_norm(x, w, residual=r)
+    (y.float().square().sum() + s.float().sum()).backward(retain_graph=True)
+    first = x.grad.clone(), w.grad.clone()
+    assert torch.equal(x.grad, r.grad)
+    x.grad.zero_()
+    assert torch.equal(r.grad, first[0])
+    (y.float().square().sum() + s.float().sum()).backward()
+    assert torch.equal(x.grad, first[0]) and torch.equal(r.grad, first[0] + first[0]) and torch.equal(w.grad, first[1] + first[1])
+
+
+def test_nothing_is_kept_without_gradients(fp8q):
+    x, w = rand(512, 1024), rand(2048, 1024)
+    plain = fp8q.gated_linear_fp8(x, w)
+    assert not plain.requires_grad
+    w.requires_grad_(True)
+    with torch.no_grad():
+        assert not fp8q.gated_linear_fp8(x, w).requires_grad and not fp8q.rms_norm(x, w[0]).requires_grad
+    h = fp8q.gated_linear_fp8(x, w)
+    assert h.requires_grad and torch.equal(h.detach(), plain)
+    (dw,) = torch.autograd.grad(h, w, torch.ones_like(h))
+    assert dw.shape == w.shape
+
+
+def test_a_second_derivative_is_refused(fp8q):
+    x, w = rand(8, 128).requires_grad_(True), rand(128).requires_grad_(True)
+    wide = rand(64, 128, seed=2).requires_grad_(True)
+    for f in (lambda: fp8q.rms_norm(x, w), lambda: fp8q.gated_linear_fp8(x, wide)):
+        y = f()
+        (g,) = torch.autograd.grad(y, x, torch.ones_like(y), create_graph=True)
+        (plain,) = torch.autograd.grad(f(), x, torch.ones_like(y))
+        assert torch.equal(g.detach(), plain)
+        with pytest.raises(RuntimeError, match="twice"):
+            g.sum().backward()
+
+
+def test_changed_inputs_are_noticed(fp8q):
+    """An input that the backward pass reads may not be written in between."""
+    x, w = rand(8, 128).requires_grad_(True), rand(128).requires_grad_(True)
+    y = fp8q.rms_norm(x, w)
+    with torch.no_grad():
+        w.add_(1)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        torch.autograd.grad(y, x, torch.ones_like(y))
+
+
+def test_training_steps_in_graphs(fp8q):
+    """A block's forward and backward captured twice (two graphs, each with its own workspaces) and
+    replayed in turn on new inputs gives the eager step's bits.  No eager graph of the leaves may
+    live while a backward pass is captured: torch then orders the capture after that graph's
+    stream, whatever the operators are, and the capture fails."""
+    x, res, nw = rand(96, 256), rand(96, 256, seed=1), rand(256, seed=2)
+    wg, wd = rand(256, 256, seed=3) / 16, rand(256, 128, seed=4) / 16
+    leaves = [t.requires_grad_(True) for t in (x, res, nw, wg, wd)]
+
+    def step():
+        y, r = fp8q.rms_norm(x, nw, residual=res)
+        out = fp8q.ffn_fp8(y, wg, wd) + r
+        return (out.detach(), *torch.autograd.grad(out, leaves, torch.ones_like(out)))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graphs = []
+    with torch.cuda.stream(side):
+        step()
+        for _ in range(2):
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=side):
+                out = step()
+            graphs.append((graph, out))
+    torch.cuda.current_stream().wait_stream(side)
+    for i in range(4):
+        with torch.no_grad():
+            x.copy_(rand(96, 256, seed=10 + i))
+            res.copy_(rand(96, 256, seed=20 + i))
+        graph, out = graphs[i % 2]
+        graph.replay()
+        got = [t.clone() for t in out]
+        for a, b in zip(got, step()):
+            assert torch.equal(a, b)
