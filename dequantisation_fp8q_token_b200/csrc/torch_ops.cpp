@@ -310,6 +310,12 @@ void gated_mm_blockwise_quant(const Tensor& a, const Tensor& scale_a, const Tens
           "fp8q_gated_mm_blockwise_quant");
 }
 
+int64_t rows_before_last(at::IntArrayRef shape) {
+    int64_t rows = 1;
+    for (size_t i = 0; i + 1 < shape.size(); ++i) rows *= shape[i];
+    return rows;
+}
+
 // Parts of one buffer, each at a multiple of 256 bytes
 template <size_t N>
 struct Parts {
@@ -346,7 +352,7 @@ struct GatedLinear : torch::autograd::Function<GatedLinear> {
         const fp8q_stream_t st = on_device(x_in, w_in);
         const fp8q_dtype dt = dtype_code(x_in, "input");
         const Tensor x = x_in.contiguous(), w = w_in.contiguous();
-        const int64_t I = w.size(0) / 2, K = w.size(1), T = K ? x.numel() / K : 0;
+        const int64_t I = w.size(0) / 2, K = w.size(1), T = rows_before_last(x.sizes());
         std::vector<int64_t> shape = x.sizes().vec();
         shape.back() = I;
         Tensor h = at::empty(shape, x.options());
@@ -383,8 +389,7 @@ struct GatedLinear : torch::autograd::Function<GatedLinear> {
         const std::vector<int64_t> x_shape = ctx->saved_data["x_shape"].toIntVector();
         const std::vector<int64_t> w_shape = ctx->saved_data["w_shape"].toIntVector();
         const int64_t I = w_shape[0] / 2, K = w_shape[1];
-        int64_t T = K ? 1 : 0;
-        for (size_t i = 0; K && i + 1 < x_shape.size(); ++i) T *= x_shape[i];
+        const int64_t T = rows_before_last(x_shape);
         const Parts<6> at_ = parts(T, I, K, dh.element_size(), true);
         uint8_t* b = static_cast<uint8_t*>(buf.data_ptr());
         const uint8_t *x8 = b + at_.at[0], *w8 = b + at_.at[1];

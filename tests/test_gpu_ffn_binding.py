@@ -89,6 +89,14 @@ def test_empty_inputs(fp8q):
     assert h.shape == (0, 32)
     dx, dw = torch.autograd.grad(h, (x, wide), h.detach())
     assert dx.shape == (0, 256) and dw.shape == (64, 256) and (dw == 0).all()
+    # no products to sum: zeros, whatever the memory held
+    x, none = rand(2, 5, 0).requires_grad_(True), rand(64, 0).requires_grad_(True)
+    del h
+    torch.full((1 << 16,), float("nan"), device="cuda", dtype=BF16)
+    h = fp8q.gated_linear_fp8(x, none)
+    assert h.shape == (2, 5, 32) and (h == 0).all()
+    dx, dw = torch.autograd.grad(h, (x, none), torch.ones_like(h))
+    assert dx.shape == (2, 5, 0) and dw.shape == (64, 0)
 
 
 def test_gradients_of_leaves_are_their_own(fp8q):
