@@ -524,15 +524,15 @@ gated_mm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
 
     if constexpr (kSingle) {
         // The one tile of this CTA or cluster: rank r finishes rows [r * share, (r + 1) * share)
-        // of the live ones.  This CTA's copies and MMAs are done (drained above), so past the
-        // barrier its ring holds nothing and takes its sums, row by row.
+        // of the live ones.  A warp that has folded this CTA's last k-block has seen its last MMA
+        // and, before that, its last copy complete, so the ring holds nothing and takes the sums,
+        // row by row.
         int mb, nb;
         tile_coords(first, p.tiles_m, p.tiles_n, mb, nb);
         const int live = min(BM, p.M - mb * BM);
         const int share = (live + split - 1) / split;
-        __syncthreads();
         const int trow = row_of(), tcol = col_of();
-        if (warp >= 2 && trow < live) {
+        if (warp >= 2 && trow < live && !fail) {
             float* dst = reinterpret_cast<float*>(smem) + trow * kPartPitch + tcol;
 #pragma unroll
             for (int i = 0; i < kCols / 2; ++i)
@@ -542,77 +542,95 @@ gated_mm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
         __syncwarp();
         if (split > 1) pair::cluster_sync();
         else __syncthreads();
-        if (warp >= 2) {
-            for (int r = warp - 2; r < share && rank * share + r < live; r += kEpiWarps) {
-                const int row = mb * BM + rank * share + r;
-                // lane l: columns 4 l .. 4 l + 3, the ranks' sums added in rank order
-                const uint32_t mine = smem_u32(smem) + 4u * static_cast<uint32_t>((rank * share + r) * kPartPitch + 4 * lane);
-                float4 a[kMaxSplit], b[kMaxSplit];
+        // no CTA leaves while another may still read its sums: each warp arrives once it has read
+        // all that it will, and waits at the end
+        bool arrived = split == 1;
+        const int mine = min(share, live - rank * share);         // rows of this rank
+        for (int r = warp - 2; r < mine && warp >= 2; r += kEpiWarps) {
+            // lane l: columns 4 l .. 4 l + 3, the ranks' sums added in rank order.  One row at a
+            // time: two or four in flight made the code larger and the kernel slower (128 x 2048 x
+            // 7168: 16.0 against 16.9 us; 1 x 2048 x 7168: 10.1 against 10.3).
+            const uint32_t at = smem_u32(smem) + 4u * static_cast<uint32_t>((rank * share + r) * kPartPitch + 4 * lane);
+            float4 a[kMaxSplit], b[kMaxSplit];
 #pragma unroll
-                for (int s = 0; s < kMaxSplit; ++s) {
-                    if (s < split) {
-                        uint32_t src = mine;
-                        if (split > 1) asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(src) : "r"(mine), "r"(s));
-                        a[s] = ld_cluster16(src);
-                        b[s] = ld_cluster16(src + 4u * kHN);
-                    }
-                }
-                float g[4] = {0.0f, 0.0f, 0.0f, 0.0f}, u[4] = {0.0f, 0.0f, 0.0f, 0.0f}, h[4];
-#pragma unroll
-                for (int s = 0; s < kMaxSplit; ++s) {
-                    if (s < split) {
-                        g[0] += a[s].x; g[1] += a[s].y; g[2] += a[s].z; g[3] += a[s].w;
-                        u[0] += b[s].x; u[1] += b[s].y; u[2] += b[s].z; u[3] += b[s].w;
-                    }
-                }
-                activate(g, u, p.act, h);
-                const int col = nb * kHN + 4 * lane;
-                if constexpr (OUT != kOutQuant) {
-                    auto put = [&](void* base, int64_t at, int align, const float (&v)[4]) {
-                        T* d = static_cast<T*>(base) + at;
-                        if (align >= 16 && col + 4 <= p.I) {
-                            if constexpr (YT == kF32) st_v4(d, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]),
-                                                                          __float_as_uint(v[2]), __float_as_uint(v[3])));
-                            else st_v2(d, make_uint2(pack2<YT>(v[0], v[1]), pack2<YT>(v[2], v[3])));
-                            return;
-                        }
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            if (col + i >= p.I) break;
-                            if constexpr (YT == kF32) d[i] = v[i];
-                            else if constexpr (YT == kF16) d[i] = __float2half_rn(v[i]);
-                            else d[i] = __float2bfloat16_rn(v[i]);
-                        }
-                    };
-                    put(p.h, static_cast<int64_t>(row) * p.I + col, p.align_h, h);
-                    if (!FINE && p.gu) {
-                        put(p.gu, static_cast<int64_t>(row) * 2 * p.I + col, p.align_gu, g);
-                        put(p.gu, static_cast<int64_t>(row) * 2 * p.I + p.I + col, p.align_gu, u);
-                    }
-                } else {
-                    uint32_t a = absmax_of(h);
-#pragma unroll
-                    for (int off = 16; off > 0; off >>= 1) a = max(a, __shfl_xor_sync(0xFFFFFFFFu, a, off));
-                    float scale, sinv;
-                    group_scales(a, p.fmt, p.rule, scale, sinv);
-                    if (lane == 0) p.sinv[static_cast<int64_t>(row) * p.groups + nb] = sinv;
-                    const uint32_t w = encode4(h, scale, p.fmt);
-                    uint8_t* d = p.q + static_cast<int64_t>(row) * p.I + col;
-                    if (p.align_q >= 4 && col + 4 <= p.I) st_u32(d, w);
-                    else
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (col + i < p.I) d[i] = static_cast<uint8_t>(w >> (8 * i));
+            for (int s = 0; s < kMaxSplit; ++s) {
+                if (s < split) {
+                    uint32_t src = at;
+                    if (split > 1) asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(src) : "r"(at), "r"(s));
+                    a[s] = ld_cluster16(src);
+                    b[s] = ld_cluster16(src + 4u * kHN);
                 }
             }
+            float g[4] = {0.0f, 0.0f, 0.0f, 0.0f}, u[4] = {0.0f, 0.0f, 0.0f, 0.0f}, h[4];
+#pragma unroll
+            for (int s = 0; s < kMaxSplit; ++s) {
+                if (s < split) {
+                    g[0] += a[s].x; g[1] += a[s].y; g[2] += a[s].z; g[3] += a[s].w;
+                    u[0] += b[s].x; u[1] += b[s].y; u[2] += b[s].z; u[3] += b[s].w;
+                }
+            }
+            if (!arrived && r + kEpiWarps >= mine) {
+                __syncwarp();
+                // the operands: not before the loads have returned
+                asm volatile("barrier.cluster.arrive.release.aligned;"
+                             :: "f"(g[0]), "f"(g[1]), "f"(g[2]), "f"(g[3]), "f"(u[0]), "f"(u[1]), "f"(u[2]), "f"(u[3])
+                             : "memory");
+                arrived = true;
+            }
+            activate(g, u, p.act, h);
+            const int64_t row = static_cast<int64_t>(mb) * BM + rank * share + r;
+            const int col = nb * kHN + 4 * lane;
+            if constexpr (OUT != kOutQuant) {
+                auto put = [&](void* base, int64_t o, int align, const float (&v)[4]) {
+                    T* d = static_cast<T*>(base) + o;
+                    if (align >= 16 && col + 4 <= p.I) {
+                        if constexpr (YT == kF32) st_v4(d, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]),
+                                                                      __float_as_uint(v[2]), __float_as_uint(v[3])));
+                        else st_v2(d, make_uint2(pack2<YT>(v[0], v[1]), pack2<YT>(v[2], v[3])));
+                        return;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (col + i >= p.I) break;
+                        if constexpr (YT == kF32) d[i] = v[i];
+                        else if constexpr (YT == kF16) d[i] = __float2half_rn(v[i]);
+                        else d[i] = __float2bfloat16_rn(v[i]);
+                    }
+                };
+                put(p.h, row * p.I + col, p.align_h, h);
+                if (!FINE && p.gu) {
+                    put(p.gu, row * 2 * p.I + col, p.align_gu, g);
+                    put(p.gu, row * 2 * p.I + p.I + col, p.align_gu, u);
+                }
+            } else {
+                uint32_t amax = absmax_of(h);
+#pragma unroll
+                for (int off = 16; off > 0; off >>= 1) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, off));
+                float scale, sinv;
+                group_scales(amax, p.fmt, p.rule, scale, sinv);
+                if (lane == 0) p.sinv[row * p.groups + nb] = sinv;
+                const uint32_t w = encode4(h, scale, p.fmt);
+                uint8_t* d = p.q + row * p.I + col;
+                if (p.align_q >= 4 && col + 4 <= p.I) {
+                    st_u32(d, w);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (col + i < p.I) d[i] = static_cast<uint8_t>(w >> (8 * i));
+                }
+            }
+        }
+        if (!arrived) {
+            __syncwarp();
+            asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
         }
     }
 
     if (fail && p.status && lane == 0) atomicOr(p.status, fail);
     tc_fence_before();
-    if (kSingle && split > 1) {                      // no CTA leaves while another may still read its sums
+    if (kSingle && split > 1) {
         __syncwarp();
-        pair::cluster_sync();
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     }
     __syncthreads();
     tc_fence_after();
@@ -893,18 +911,18 @@ int split_fit(int size) {
 
 // Split the k axis over the CTAs of a cluster where that is estimated to be faster: a tile
 // whose k axis one SM walks alone streams its weights at that SM's rate while others idle.
-// In ns, from runs of 512 to 2048 columns: a k-block takes 480 (fine scales), 380 (fine
-// scales, DUP) or 330; a cluster's barriers take 1000 and its exchange 37 for each row that a
-// CTA receives parts of (14 bytes a clock through distributed shared memory); an undivided
-// tile's own epilogue takes 1200, what finishing a DUP tile takes is the same either way.
-// 128 x 2048 x 2048: 14.1 us undivided, 11.6 on 4 CTAs; 128 x 512 x 1024: 8.8 and 9.1;
-// 1 x 2048 x 7168: 25.3 undivided, 10.5 on 6.
+// In ns, from runs of 512 to 2048 columns over every split: a k-block takes 480 (fine scales),
+// 380 (fine scales, DUP) or 330.  A cluster's barriers and its first rows take 1500, and each
+// row that a CTA reads parts of 37 (14 bytes a clock through distributed shared memory).  An
+// undivided tile's own epilogue takes 1200, or (DUP) 550 for each eight rows.
+// Undivided and at the best split, us: 64 x 1024 x 1024 10.9 and 7.0 (4 CTAs), 100 x 1024 x 1024
+// 8.4 and 8.9 (4), 128 x 512 x 2048 12.0 and 10.0 (8), 1 x 2048 x 7168 25.5 and 10.2 (6).
 int choose_split(const GatedParams& p, int64_t per_kb, bool dup) {
     const int tiles = p.tiles_m * p.tiles_n, rows = p.M < BM ? p.M : BM;
     int split = 1;
-    int64_t best = per_kb * p.num_kb + (dup ? 0 : 1200);
+    int64_t best = per_kb * p.num_kb + (dup ? 550 * ((rows + 7) / 8) : 1200);
     for (int c = 2; c <= kMaxSplit && c <= p.num_kb && static_cast<int64_t>(tiles) * c <= sm_count(); ++c) {
-        const int64_t cost = per_kb * ((p.num_kb + c - 1) / c) + 1000 + 37LL * rows * (c - 1) / c;
+        const int64_t cost = per_kb * ((p.num_kb + c - 1) / c) + 1500 + 37LL * rows * (c - 1) / c;
         if (cost >= best || tiles > split_fit(c)) continue;
         best = cost;
         split = c;
