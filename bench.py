@@ -982,9 +982,9 @@ OP_SOURCES = {
     "block_dequant": ["dequant.cu", "fp8q_device.cuh"],
     "cast_from_fp8_group": ["dequant.cu", "fp8q_device.cuh"],
     "block_dequant_grouped": ["dequant.cu", "fp8q_device.cuh"],
-    "cast_per_channel": ["quant_scaled.cu", "fp8q_device.cuh"],
-    "cast_per_tensor_f32_e5m2": ["quant_scaled.cu", "fp8q_device.cuh"],
-    "cast_per_tensor_f16_zero": ["quant_scaled.cu", "fp8q_device.cuh"],
+    "cast_per_channel": ["quant_scaled.cu", "per_tensor_device.cuh", "fp8q_device.cuh"],
+    "cast_per_tensor_f32_e5m2": ["quant_scaled.cu", "per_tensor_device.cuh", "fp8q_device.cuh"],
+    "cast_per_tensor_f16_zero": ["quant_scaled.cu", "per_tensor_device.cuh", "fp8q_device.cuh"],
 }
 
 

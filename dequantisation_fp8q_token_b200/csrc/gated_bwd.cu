@@ -13,7 +13,8 @@
 // element of dh for 16-bit types; writing the gradients in between would move
 // 16 and round them once more.  Pass 2 walks the rows from the end, where
 // pass 1 left its last inputs in L2.
-#include "fp8q_device.cuh"
+#include "gated_device.cuh"
+#include "per_tensor_device.cuh"
 #include "fp8q_internal.h"
 
 namespace fp8q {

@@ -32,6 +32,7 @@
 //     rows of Wg and the odd one its rows of Wu.
 #include <cstring>
 
+#include "gated_device.cuh"
 #include "mm_device.cuh"
 
 namespace fp8q {

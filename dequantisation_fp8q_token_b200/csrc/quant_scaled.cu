@@ -15,7 +15,7 @@
 // cast.  Pass 1 reads the last kL2KeepBytes of x with an L2 evict_last policy
 // (the rest evict_first), and pass 2 walks the tensor from the end, so the
 // second read of that tail comes from L2 instead of HBM.
-#include "fp8q_device.cuh"
+#include "per_tensor_device.cuh"
 #include "fp8q_internal.h"
 
 namespace fp8q {
