@@ -162,11 +162,13 @@ struct FwdParams {
 // and blockDim.x is a multiple of 32, so a group of G elements is 2^lanes_log2
 // consecutive lanes of one warp and its amax takes lanes_log2 shuffles.
 // FMT: kE4M3 or kE5M2 (codes, and y if it is wanted too), or kNoCast (y only).
-// bf16 4096 x 7168 with a residual: 38.1 us to y (94% of the measured copy
-// bandwidth), 38.7 us to e4m3 (81%), where the group's amax, its two divisions
-// and the cast add half again to the instructions (20 against 14 million).  A
-// persistent form that kept rows in flight in a shared-memory ring took 44 and
-// 59 us: its 16-byte vectors double the work per group.
+// bf16 4096 x 7168 with a residual: 36.3 us to y (99% of the measured copy
+// bandwidth), 33.1 us to e4m3 (95%); without one, where half the bytes move,
+// 21.4 us (84%) and 22.4 us (60%): there the instructions are the bound, of
+// which the group's amax, its two divisions and the cast add half again (20
+// against 14 million at that size).  A persistent form that kept rows in
+// flight in a shared-memory ring took 44 and 59 us: its 16-byte vectors double
+// the work per group.
 // ---------------------------------------------------------------------------
 constexpr int kNoCast = 2;
 
@@ -649,7 +651,11 @@ fp8q_status run_fwd(const FwdParams& p0, cudaStream_t s) {
     }
     const int64_t nvec = p.n * ES / vb;
     if (vb == 32) {
-        if (nvec <= 1024) return run_fwd_vec<XT, WT, 32, 1>(p, s);
+        // One vector a thread has the shorter latency; two leave room for more and smaller CTAs
+        // an SM, whose rows then overlap better: bf16 7168 wide to fp8, 300 rows 5.0 and 5.4 us,
+        // 1000 rows 11.2 and 10.7, 4096 rows 38.8 and 33.1.  Four were slower (39.3).
+        const bool many = p.m >= 3LL * sm_count();
+        if (nvec <= 256 || (nvec <= 1024 && !many)) return run_fwd_vec<XT, WT, 32, 1>(p, s);
         if (nvec <= 2048) return run_fwd_vec<XT, WT, 32, 2>(p, s);
         if constexpr (XT == kF32) return run_fwd_vec<XT, WT, 32, 4>(p, s);
         return FP8Q_ERR_CUDA;      // not reached: 16-bit rows of more vectors take 16-byte ones
