@@ -536,9 +536,8 @@ fp8q_status fp8q_rms_norm_bwd(const void* dy, const void* r, fp8q_dtype xt, cons
     if (!aligned(dy, es) || !aligned(r, es) || !aligned(dres, es) || !aligned(dx, es) || !aligned(weight, ws) ||
         !aligned(dweight, ws) || !aligned(rstd, 4))
         return FP8Q_ERR_MISALIGNED;
-    if (m > 0 && dweight &&
-        (!workspace || !aligned(workspace, 16) || workspace_bytes < rms_norm_bwd_workspace(m, n)))
-        return FP8Q_ERR_WORKSPACE;
+    const size_t scratch = dweight ? rms_norm_bwd_workspace(m, n) : 0;
+    if (scratch > 0 && (!workspace || !aligned(workspace, 16) || workspace_bytes < scratch)) return FP8Q_ERR_WORKSPACE;
     return launch_rms_norm_bwd(dy, r, xt, weight, wt, rstd, dres, m, n, dx, dweight, static_cast<float*>(workspace),
                                reinterpret_cast<cudaStream_t>(stream));
 }

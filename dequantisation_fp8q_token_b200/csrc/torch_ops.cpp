@@ -218,12 +218,12 @@ struct RmsNorm : torch::autograd::Function<RmsNorm> {
             dw = at::empty_like(weight);
             // a workspace of this call's own: the caching allocator orders it by stream and by graph
             bytes = fp8q_rms_norm_bwd_workspace_bytes(m, n);
-            workspace = at::empty({static_cast<int64_t>(bytes)}, r.options().dtype(at::kByte));
+            if (bytes) workspace = at::empty({static_cast<int64_t>(bytes)}, r.options().dtype(at::kByte));
         }
         check(fp8q_rms_norm_bwd(dy.data_ptr(), r.data_ptr(), dtype_code(r, "x"), weight.data_ptr(),
                                 dtype_code(weight, "weight"), rstd.data_ptr<float>(), dr.defined() ? dr.data_ptr() : nullptr,
                                 m, n, dx.data_ptr(), dw.defined() ? dw.data_ptr() : nullptr,
-                                dw.defined() ? workspace.data_ptr() : nullptr, bytes, st),
+                                bytes ? workspace.data_ptr() : nullptr, bytes, st),
               "fp8q_rms_norm_bwd");
         return once({dx, dw, has_residual ? dx : Tensor(), Tensor()}, graph, "rms_norm");
     }

@@ -565,8 +565,8 @@ fp8q_status fp8q_rms_norm_quant(const void* x, fp8q_dtype xt, const void* residu
  *   dres may be NULL (r is not used further).  rstd: fp32 [m], the forward's.
  * dweight: [n] of type wt, or NULL when it is not wanted.
  * workspace: fp8q_rms_norm_bwd_workspace_bytes(m, n) bytes (asked on the
- *   device of the call), 16-byte aligned, when dweight is given; scratch, as
- *   fp8q_cast_per_tensor's.  Sums are fp32 in a fixed order, without atomics.
+ *   device of the call; 0 for few rows), 16-byte aligned, when dweight is given;
+ *   scratch, as fp8q_cast_per_tensor's.  Sums are fp32 in a fixed order, without atomics.
  * The outputs must not overlap the inputs.  m == 0 writes zeros to dweight.
  */
 size_t fp8q_rms_norm_bwd_workspace_bytes(int64_t m, int64_t n);

@@ -267,3 +267,29 @@ def test_side_stream_and_graph_replay(fp8q):
     step()
     for a, b in zip(got, (q, s, ro, dx, dw)):
         assert torch.equal(a, b)
+
+
+# more rows than the one-launch backward pass takes, one vector a thread and more, widths that end
+# inside a vector, and no vectors at all; and the forward's form for many wide rows
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("res", [False, True])
+@pytest.mark.parametrize("m,n", [(512, 520), (513, 520), (513, 4096), (600, 7168), (514, 7176), (520, 18432), (515, 20488),
+                                 (700, 33), (513, 1001), (5000, 8)])
+def test_backward_many_rows(fp8q, dt, res, m, n):
+    check_backward(fp8q, m, n, dt, res)
+
+
+@pytest.mark.parametrize("m", [300, 600])
+def test_backward_many_rows_fp32_weight_and_unaligned(fp8q, m):
+    check_backward(fp8q, m, 2048, BF16, True, w32=True)
+    check_backward(fp8q, m, 999, F16, False, w32=True)
+    for dt, offset in ((BF16, 1), (F32, 2)):
+        check_backward(fp8q, m, 1024, dt, True, offset=offset)
+
+
+@pytest.mark.parametrize("m,n,group", [(443, 7168, 128), (444, 7168, 128), (500, 4112, 16), (450, 16384, 128),
+                                       (446, 8192, 256), (600, 5120, 64)])
+def test_forward_many_wide_rows(fp8q, m, n, group):
+    for dt, res in ((BF16, True), (F16, False), (F32, True)):
+        x, r, w = make(m, n, dt, res)
+        check_forward(fp8q, x, r, w, group)
