@@ -177,6 +177,8 @@ def lib() -> ctypes.CDLL:
             L.fp8q_rms_norm_bwd_workspace_bytes.argtypes = [i64, i64]
             L.fp8q_rms_norm_bwd.restype = st
             L.fp8q_rms_norm_bwd.argtypes = [p, p, i32, p, i32, p, p, i64, i64, p, p, p, sz, p]
+            L.fp8q_cast_per_tensor_pair.restype = st
+            L.fp8q_cast_per_tensor_pair.argtypes = [p, i64, p, p, p, i64, p, p, i32, i32, p, sz, i32, p]
             L.fp8q_gated_mm.restype = st
             L.fp8q_gated_mm.argtypes = [p, i32, p, p, i32, i64, i64, i64, p, p, p, i32, i32, p, p, p, p]
             L.fp8q_gated_mm_blockwise.restype = st

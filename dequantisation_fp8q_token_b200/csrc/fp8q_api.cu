@@ -135,6 +135,35 @@ fp8q_status fp8q_cast_per_tensor_ex(const void* x, fp8q_dtype xt, int64_t numel,
     return launch_per_tensor(x, xt, numel, fmt, q, scale_inv, static_cast<uint32_t*>(workspace), rule, s);
 }
 
+fp8q_status fp8q_cast_per_tensor_pair(const void* x0, int64_t numel0, uint8_t* q0, float* scale_inv0, const void* x1,
+                                      int64_t numel1, uint8_t* q1, float* scale_inv1, fp8q_dtype xt, fp8q_format fmt,
+                                      void* workspace, size_t workspace_bytes, fp8q_scale_rule rule,
+                                      fp8q_stream_t stream) {
+    if (!dtype_ok(xt)) return FP8Q_ERR_BAD_DTYPE;
+    if (!rule_ok(rule)) return FP8Q_ERR_BAD_RULE;
+    if (!fmt_ok(fmt)) return FP8Q_ERR_BAD_FORMAT;
+    const void* x[2] = {x0, x1};
+    const int64_t numel[2] = {numel0, numel1};
+    uint8_t* q[2] = {q0, q1};
+    float* sinv[2] = {scale_inv0, scale_inv1};
+    for (int i = 0; i < 2; ++i) {
+        if (numel[i] < 0 || checked_mul(numel[i], dtype_bytes(xt)) < 0) return FP8Q_ERR_BAD_SHAPE;
+        if (!sinv[i] || (numel[i] > 0 && (!x[i] || !q[i]))) return FP8Q_ERR_NULL_POINTER;
+        if (!aligned(sinv[i], 4) || !aligned(x[i], dtype_bytes(xt))) return FP8Q_ERR_MISALIGNED;
+    }
+    if ((numel0 > 0 || numel1 > 0) &&
+        (!workspace || workspace_bytes < kPerTensorWorkspaceBytes || !aligned(workspace, 16)))
+        return FP8Q_ERR_WORKSPACE;
+    if (numel0 == 0 || numel1 == 0) {
+        const fp8q_status st = fp8q_cast_per_tensor_ex(x0, xt, numel0, fmt, q0, scale_inv0, workspace, workspace_bytes,
+                                                       rule, stream);
+        if (st != FP8Q_OK) return st;
+        return fp8q_cast_per_tensor_ex(x1, xt, numel1, fmt, q1, scale_inv1, workspace, workspace_bytes, rule, stream);
+    }
+    return launch_per_tensor_pair(x, numel, q, sinv, xt, fmt, static_cast<uint32_t*>(workspace), rule,
+                                  reinterpret_cast<cudaStream_t>(stream));
+}
+
 fp8q_status fp8q_tensor_amax(const void* x, fp8q_dtype xt, int64_t numel, uint32_t* amax_bits, void* workspace,
                              size_t workspace_bytes, fp8q_stream_t stream) {
     if (!dtype_ok(xt)) return FP8Q_ERR_BAD_DTYPE;

@@ -361,12 +361,9 @@ struct GatedLinear : torch::autograd::Function<GatedLinear> {
         uint8_t* b = static_cast<uint8_t*>(buf.data_ptr());
         uint8_t *x8 = b + at_.at[0], *w8 = b + at_.at[1];
         auto *sx = reinterpret_cast<float*>(b + at_.at[2]), *sw = reinterpret_cast<float*>(b + at_.at[3]);
-        check(fp8q_cast_per_tensor_ex(x.data_ptr(), dt, T * K, FP8Q_E4M3FN, x8, sx, b + at_.at[4], cast_workspace(),
-                                      FP8Q_SCALE_IEEE, st),
-              "fp8q_cast_per_tensor");
-        check(fp8q_cast_per_tensor_ex(w.data_ptr(), dt, 2 * I * K, FP8Q_E4M3FN, w8, sw, b + at_.at[4], cast_workspace(),
-                                      FP8Q_SCALE_IEEE, st),
-              "fp8q_cast_per_tensor");
+        check(fp8q_cast_per_tensor_pair(x.data_ptr(), T * K, x8, sx, w.data_ptr(), 2 * I * K, w8, sw, dt, FP8Q_E4M3FN,
+                                        b + at_.at[4], cast_workspace(), FP8Q_SCALE_IEEE, st),
+              "fp8q_cast_per_tensor_pair");
         check(fp8q_gated_mm(x8, FP8Q_E4M3FN, w8, w8 + I * K, FP8Q_E4M3FN, T, I, K, sx, sw, sw,
                             static_cast<fp8q_activation>(act), dt, h.data_ptr(), keep ? b + at_.at[5] : nullptr, nullptr, st),
               "fp8q_gated_mm");

@@ -3,7 +3,7 @@ calls that a step makes between launches (the norms, the fine-grained gated prod
 functions) have theirs in C++ (csrc/torch_ops.cpp), where it costs a third.
 
 Entry points with the C names (caller-provided outputs, nothing allocated):
-    fp8q_rms_norm_quant, fp8q_rms_norm_bwd
+    fp8q_rms_norm_quant, fp8q_rms_norm_bwd, fp8q_cast_per_tensor_pair
     fp8q_gated_mm, fp8q_gated_mm_blockwise, fp8q_gated_mm_blockwise_quant, fp8q_gated_bwd_cast
 
 Allocating helpers:
@@ -25,7 +25,7 @@ from . import (E4M3FN, E5M2, SCALE_IEEE, _FMT_DTYPE, _FP8_DTYPES, _check, _dev_p
 __all__ = [
     "fp8q_rms_norm_quant", "fp8q_rms_norm_bwd", "fp8q_rms_norm_bwd_workspace_bytes",
     "rms_norm", "rms_norm_cast_to_fp8",
-    "ACT_SILU", "ACT_GELU_TANH", "fp8q_gated_mm", "fp8q_gated_mm_blockwise", "fp8q_gated_mm_blockwise_quant",
+    "fp8q_cast_per_tensor_pair", "ACT_SILU", "ACT_GELU_TANH", "fp8q_gated_mm", "fp8q_gated_mm_blockwise", "fp8q_gated_mm_blockwise_quant",
     "fp8q_gated_bwd_cast", "gated_linear_fp8", "gated_linear_fp8_blockwise", "ffn_fp8", "ffn_fp8_blockwise",
 ]
 
@@ -134,6 +134,24 @@ def _act_of(act) -> int:
     if isinstance(act, str):
         return {"silu": ACT_SILU, "gelu_tanh": ACT_GELU_TANH}[act]
     return int(act)
+
+
+def fp8q_cast_per_tensor_pair(x0: torch.Tensor, q0: torch.Tensor, scale_inv0: torch.Tensor, x1: torch.Tensor,
+                              q1: torch.Tensor, scale_inv1: torch.Tensor, workspace: torch.Tensor, fmt=E4M3FN,
+                              rule=SCALE_IEEE, stream=None) -> None:
+    """fp8q_cast_per_tensor_ex of two tensors of one dtype (a product's operands), with the same bytes, in two
+    launches where both fit in L2 together; workspace as fp8q_cast_per_tensor's."""
+    if x0.dtype != x1.dtype:
+        raise TypeError("the two tensors must have one dtype")
+    dev = x0.device
+    for q, s, x in ((q0, scale_inv0, x0), (q1, scale_inv1, x1)):
+        _need(q, x.numel(), "q", byte=True)
+        _need(s, 1, "scale_inv", dtype=torch.float32)
+    _check(lib().fp8q_cast_per_tensor_pair(
+        _dev_ptr(x0, "x0"), x0.numel(), _dev_ptr(q0, "q0", dev), _dev_ptr(scale_inv0, "scale_inv0", dev),
+        _dev_ptr(x1, "x1", dev), x1.numel(), _dev_ptr(q1, "q1", dev), _dev_ptr(scale_inv1, "scale_inv1", dev),
+        _dtype_code(x0, "x0"), _fmt_of(fmt), _dev_ptr(workspace, "workspace", dev),
+        workspace.numel() * workspace.element_size(), _rule_of(rule), _stream(stream, dev)), "fp8q_cast_per_tensor_pair")
 
 
 def _fmt_or_none(fmt) -> Optional[int]:

@@ -198,6 +198,17 @@ fp8q_status fp8q_cast_per_tensor_ex(const void* x, fp8q_dtype xt, int64_t numel,
                                     fp8q_stream_t stream);
 
 /*
+ * The per-tensor casts of two tensors of one type, as a product's operands
+ * need them: fp8q_cast_per_tensor_ex of each, with the same bytes, in two
+ * kernels where both tensors fit in L2 together.  workspace and errors as
+ * fp8q_cast_per_tensor_ex; nothing is written when either is refused.
+ */
+fp8q_status fp8q_cast_per_tensor_pair(const void* x0, int64_t numel0, uint8_t* q0, float* scale_inv0,
+                                      const void* x1, int64_t numel1, uint8_t* q1, float* scale_inv1,
+                                      fp8q_dtype xt, fp8q_format fmt, void* workspace, size_t workspace_bytes,
+                                      fp8q_scale_rule rule, fp8q_stream_t stream);
+
+/*
  * Per-tensor cast without a caller workspace.  The paper has no counterpart:
  * this entry point is a convenience of this library, not part of the method.
  * Same computation and bytes as fp8q_cast_per_tensor, for callers that

@@ -113,6 +113,24 @@ def test_gated_bwd_validation(L):
     assert f(w=None) == 6 and f(nb=ws - 1) == 6 and f(w=A + 8) == 6
 
 
+def test_cast_pair_validation(L):
+    def f(x0=P, n0=64, q0=P, s0=P, x1=P, n1=64, q1=P, s1=P, xt=2, fmt=0, w=A, nb=8192, rule=0):
+        return L.fp8q_cast_per_tensor_pair(x0, n0, q0, s0, x1, n1, q1, s1, xt, fmt, w, nb, rule, None)
+    assert f(xt=5) == 2 and f(rule=2) == 10 and f(fmt=4) == 3
+    assert f(n0=-1) == 4 and f(n1=-1) == 4 and f(n1=1 << 62) == 4
+    assert f(x0=None) == 1 and f(q0=None) == 1 and f(s0=None) == 1 and f(x1=None) == 1 and f(q1=None) == 1 and f(s1=None) == 1
+    assert f(s0=P + 2) == 5 and f(s1=P + 1) == 5 and f(x0=P + 1) == 5 and f(x1=P + 1) == 5
+    assert f(w=None) == 6 and f(nb=8191) == 6 and f(w=A + 8) == 6
+    import dequantisation_fp8q_token_b200 as b
+    x, q, s, ws = torch.zeros(64), torch.zeros(64, dtype=torch.uint8), torch.zeros(1), torch.zeros(8192, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="CUDA"):
+        b.fp8q_cast_per_tensor_pair(x, q, s, x, q, s, ws)
+    with pytest.raises(ValueError):
+        b.fp8q_cast_per_tensor_pair(x, q, s, x, q[:3], s, ws)
+    with pytest.raises(TypeError):
+        b.fp8q_cast_per_tensor_pair(x, q, s, x.half(), q, s, ws)
+
+
 def test_gated_binding_refuses(L):
     import dequantisation_fp8q_token_b200 as f
     e4 = torch.float8_e4m3fn

@@ -56,6 +56,30 @@ def test_status_errors_and_refusals(fp8q):
             call()
 
 
+@pytest.mark.parametrize("dt", [BF16, torch.float16, torch.float32])
+@pytest.mark.parametrize("n0,n1,offset", [(300 * 1024, 768 * 1024, 0), (16, 8, 0), (8, 4 << 20, 0), (1000, 2001, 0),
+                                          (5000, 4096, 1), (0, 64, 0), (64, 0, 0), (0, 0, 0), (9 << 20, 9 << 20, 0)])
+def test_cast_pair_is_two_casts(fp8q, dt, n0, n1, offset):
+    """Bit for bit, also where one has a NaN, only zeros, or values that overflow the scale."""
+    ws = torch.empty(fp8q.fp8q_cast_per_tensor_workspace_bytes(), dtype=torch.uint8, device="cuda")
+    for fmt, rule, kind in ((0, "ieee", "plain"), (1, "torch", "plain"), (0, "ieee", "nan"), (1, "ieee", "zero"), (0, "torch", "tiny")):
+        xs = [rand(n + offset, seed=i, dt=dt)[offset:] for i, n in enumerate((n0, n1))]
+        if kind == "nan" and n1:
+            xs[1][n1 // 2] = float("nan")
+        if kind == "zero":
+            xs[0].zero_()
+        if kind == "tiny":
+            xs[0].mul_(1e-39)
+        got, want = [], []
+        for x in xs:
+            for o in (got, want):
+                o += [torch.full((x.numel(),), 7, dtype=torch.uint8, device="cuda"), torch.zeros(1, device="cuda")]
+            fp8q.fp8q_cast_per_tensor_ex(x, want[-2], want[-1], ws, fmt, rule)
+        fp8q.fp8q_cast_per_tensor_pair(xs[0], got[0], got[1], xs[1], got[2], got[3], ws, fmt, rule)
+        for a, b in zip(got, want):
+            assert torch.equal(a, b), (fmt, rule, kind)
+
+
 def test_streams_given_as_objects_and_handles(fp8q):
     x, w = rand(64, 1024), rand(1024)
     want_q, want_s = fp8q.rms_norm_cast_to_fp8(x, w)
