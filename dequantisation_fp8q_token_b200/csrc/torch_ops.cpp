@@ -2,7 +2,7 @@
 // step makes between launches: their checks, their allocations and the two
 // autograd functions, in C++ over the C ABI of libfp8q (fp8q.h).  A small
 // training step is bound by the host: forward and backward of a 16 x 256 norm
-// through autograd take 61 us here and took 102 us with the functions in
+// through autograd take 57 us here and took 102 us with the functions in
 // Python over ctypes, where a bare product and its gradient take 51.
 //
 // Raises ValueError and TypeError as the rest of the binding, and Fp8qError for
