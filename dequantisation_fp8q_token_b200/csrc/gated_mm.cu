@@ -24,9 +24,13 @@
 //     of one tile, each leaves its sums in its shared memory, and each then
 //     reads the parts of its share of the rows through distributed shared
 //     memory, adds them in rank order and finishes those rows;
-//   gated_mm_kernel, kDup2, kDup4 fine scales, at most 64 or 32 rows, a tile
-//     per CTA or cluster (DUP 2, 4): the A tile holds the rows DUP times over, so that
-//     every warp's TMEM lanes hold them and each folds 1 / DUP of the columns;
+//   gated_mm_kernel, kDup2, kDup4 fine scales, at most 64 or 32 rows, clusters:
+//     the A tile holds the rows 2 or 4 times over, so that every warp's TMEM
+//     lanes hold them and each folds 1 / DUP of the columns;
+//   gated_mm_kernel, kFew16, 32   fine scales, at most 16 or 32 rows, a tile
+//     for each SM: the operands change places (the weights' 128 rows are the
+//     MMA's M, the rows of A its N), so that no power goes into rows that there
+//     are not, and a warp folds one column of gate or of up per lane;
 //   gated_pair_kernel             per-tensor scales, many tiles: 256 rows on
 //     CTA pairs (tcgen05.mma.cta_group::2), the even CTA loading the tile's
 //     rows of Wg and the odd one its rows of Wu.
@@ -58,7 +62,7 @@ static_assert(BM * kPartPitch * 4 <= kRing * (kATileBytes + 2 * kHalfBBytes), "t
 // every register of a fold thread in use, and code for the others would spill
 // some of them: 4096 x 18432 x 7168 to fp8 takes 1080 us, and took 1200 in a
 // build with 48 bytes of spills.
-enum { kWide, kRagged, kCluster, kDup2, kDup4 };
+enum { kWide, kRagged, kCluster, kDup2, kDup4, kFew16, kFew32 };
 
 struct GatedParams {
     int M, I, num_kb;
@@ -210,6 +214,8 @@ gated_mm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
     constexpr int DUP = MODE == kDup4 ? 4 : MODE == kDup2 ? 2 : 1;
     constexpr bool kSingle = MODE >= kCluster;       // one tile per CTA or cluster, finished by exchange
     constexpr int kCols = kHalf / DUP;               // columns of gate, and of up, that a thread folds
+    constexpr bool kFew = MODE >= kFew16;
+    constexpr int kRows = MODE == kFew16 ? 16 : 32;  // kFew: rows of A (N)
     using T = typename OutT<YT>::T;
     extern __shared__ uint8_t smem_raw[];
     __shared__ int s_abort;
@@ -265,8 +271,9 @@ gated_mm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
     const int kb0 = kSingle ? static_cast<int>(static_cast<int64_t>(p.num_kb) * rank / split) : 0;
     const int kb1 = kSingle ? static_cast<int>(static_cast<int64_t>(p.num_kb) * (rank + 1) / split) : p.num_kb;
     uint32_t fail = 0;
-    // epilogue: this thread's row, kCols columns of gate then as many of up, as fp32 pairs
-    float2 accum[kCols];
+    // epilogue: this thread's row, kCols columns of gate then as many of up, or (kFew) its column of
+    // gate or of up for every row of A, as fp32 pairs
+    float2 accum[kFew ? kRows / 2 : kCols];
     // its row and first column within the tile; a warp may read TMEM lanes 32 * (warp % 4) .. + 31
     auto row_of = [&] { return (DUP == 1 ? warp & 3 : DUP == 2 ? warp & 1 : 0) * 32 + lane; };
     auto col_of = [&] { return ((warp - 2) >> 2) * kHalf + (DUP == 1 ? 0 : DUP == 2 ? (warp & 3) >> 1 : warp & 3) * kCols; };
@@ -318,9 +325,16 @@ gated_mm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
                     tc_fence_after();
                     const uint32_t a0 = smem_u32(sA + stage * kATileBytes), b0 = smem_u32(sB + stage * 2 * kHalfBBytes);
 #pragma unroll
-                    for (int j = 0; j < BK / 32; ++j)
-                        mma_f8f6f4(tmem_base + static_cast<uint32_t>(acc * kBN), smem_desc_sw128(a0 + 32 * j),
-                                   smem_desc_sw128(b0 + 32 * j), idesc, FINE ? (j > 0) : (kb > kb0 || j > 0));
+                    for (int j = 0; j < BK / 32; ++j) {
+                        const uint32_t d = tmem_base + static_cast<uint32_t>(acc * kBN);
+                        const uint64_t a = smem_desc_sw128(a0 + 32 * j), b = smem_desc_sw128(b0 + 32 * j);
+                        if constexpr (kFew) {
+                            mma_f8f6f4(d, b, a, idesc, j > 0);
+                            mma_f8f6f4(d + kHN, smem_desc_sw128(b0 + kHalfBBytes + 32 * j), a, idesc, j > 0);
+                        } else {
+                            mma_f8f6f4(d, a, b, idesc, FINE ? (j > 0) : (kb > kb0 || j > 0));
+                        }
+                    }
                     mma_commit(empty0 + 8 * stage);
                     if (++stage == kRing) { stage = 0; phase ^= 1u; }
                     if (FINE || kb + 1 == kb1) {
@@ -355,8 +369,52 @@ gated_mm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
             const bool row_ok = row < p.M;
             const bool warp_rows_live = row - lane < p.M;
 #pragma unroll
-            for (int i = 0; i < kCols; ++i) accum[i] = make_float2(0.0f, 0.0f);
-            if constexpr (FINE) {
+            for (int i = 0; i < (kFew ? kRows / 2 : kCols); ++i) accum[i] = make_float2(0.0f, 0.0f);
+            if constexpr (kFew) {
+                // lane l: the scale of row l times the block's; all of them go through the warp's
+                // staging area, one k-block's while the one before may still be read
+                const float* sb = (half == 0 ? p.sg : p.su) + static_cast<int64_t>(nb) * p.ld;
+                const float* sa = p.sa + static_cast<int64_t>(lane < p.M ? lane : p.M - 1) * p.ld;
+                float sa_next = 0.0f, sb_next = 0.0f;
+                if (kb0 < kb1) {
+                    sa_next = __ldg(sa + kb0);
+                    sb_next = __ldg(sb + kb0);
+                }
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    float* slot = stage_area + (kb & 1) * kRows;
+                    if (lane < kRows) slot[lane] = __fmul_rn(sa_next, sb_next);
+                    if (kb + 1 < kb1) {
+                        sa_next = __ldg(sa + kb + 1);
+                        sb_next = __ldg(sb + kb + 1);
+                    }
+                    __syncwarp();
+                    const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(tfull0 + 8 * acc, acc_phase, abort, p.wait_limit_ns));
+                    if (!ok) { fail = kTimeoutEpilogue; break; }
+                    tc_fence_after();
+                    const uint32_t addr = tmem_base + lane_addr + static_cast<uint32_t>(acc * kBN + half * kHN);
+                    uint32_t r[kRows];
+                    if constexpr (kRows == 16) {
+                        tmem_ld16_async(addr, r);
+                        tmem_wait16(r);
+                    } else {
+                        tmem_ld32_async(addr, r);
+                        tmem_wait32(r);
+                    }
+#pragma unroll
+                    for (int i = 0; i < kRows / 4; ++i) {
+                        const float4 sc = *reinterpret_cast<const float4*>(slot + 4 * i);
+                        accum[2 * i] = __ffma2_rn(make_float2(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1])),
+                                                  make_float2(sc.x, sc.y), accum[2 * i]);
+                        accum[2 * i + 1] = __ffma2_rn(make_float2(__uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3])),
+                                                      make_float2(sc.z, sc.w), accum[2 * i + 1]);
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(tempty0 + 8 * acc);
+                    if (++acc == kAccs) { acc = 0; acc_phase ^= 1u; }
+                }
+                if (fail) break;
+            } else if constexpr (FINE) {
                 // rows past M fold with the last row's scales; nothing reads their sums
                 const float* sa_next = p.sa + static_cast<int64_t>(row_ok ? row : p.M - 1) * p.ld + kb0;
                 const float* sg_next = p.sg + static_cast<int64_t>(nb) * p.ld + kb0;
@@ -379,7 +437,8 @@ gated_mm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
                     tc_fence_after();
                     if (warp_rows_live) {
                         // chunks of 16 columns of gate, then as many of up; the load of the
-                        // next chunk is in flight while one is folded in
+                        // next chunk is in flight while one is folded in (two in flight take the
+                        // same time: the loads' throughput beside the MMAs is the bound)
                         constexpr int kChunks = kCols / 16;
                         const uint32_t addr = tmem_base + lane_addr + static_cast<uint32_t>(acc * kBN + tcol);
                         const float2 g2 = make_float2(g1, g1), u2 = make_float2(u1, u1);
@@ -533,12 +592,20 @@ gated_mm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
         const int live = min(BM, p.M - mb * BM);
         const int share = (live + split - 1) / split;
         const int trow = row_of(), tcol = col_of();
-        if (warp >= 2 && trow < live && !fail) {
-            float* dst = reinterpret_cast<float*>(smem) + trow * kPartPitch + tcol;
+        float* parts = reinterpret_cast<float*>(smem);
+        if (warp >= 2 && !fail) {
+            if constexpr (kFew) {
+                float* dst = parts + ((warp - 2) >> 2) * kHN + (warp & 3) * 32 + lane;
 #pragma unroll
-            for (int i = 0; i < kCols / 2; ++i)
-                *reinterpret_cast<float4*>(dst + (i < kCols / 4 ? 4 * i : kHN + 4 * (i - kCols / 4))) =
-                    make_float4(accum[2 * i].x, accum[2 * i].y, accum[2 * i + 1].x, accum[2 * i + 1].y);
+                for (int r = 0; r < kRows; ++r)
+                    if (r < live) dst[r * kPartPitch] = r % 2 ? accum[r / 2].y : accum[r / 2].x;
+            } else if (trow < live) {
+                float* dst = parts + trow * kPartPitch + tcol;
+#pragma unroll
+                for (int i = 0; i < kCols / 2; ++i)
+                    *reinterpret_cast<float4*>(dst + (i < kCols / 4 ? 4 * i : kHN + 4 * (i - kCols / 4))) =
+                        make_float4(accum[2 * i].x, accum[2 * i].y, accum[2 * i + 1].x, accum[2 * i + 1].y);
+            }
         }
         __syncwarp();
         if (split > 1) pair::cluster_sync();
@@ -891,6 +958,20 @@ cudaError_t launch_gated_mode(const CUtensorMap& ma, const CUtensorMap& mg, cons
     return cudaLaunchKernelEx(&cfg, kernel, ma, mg, mu, p, idesc);
 }
 
+// The form for few rows of fine-scaled operands.  Where clusters share tiles, a fold's time is the
+// latency of its TMEM loads, and copies of the rows share those out among all warps (64 x 2048 x 7168:
+// 13.2 us, 14.0 without; with the operands swapped 14.7, since an MMA of few columns takes as long as
+// one of 256).  Where each SM has a tile, HBM sets the time and the power cap HBM's neighbours: with
+// the operands swapped 1 x 18432 x 7168 runs for seconds at 44.5 us and 1957 MHz, with copies at 51.5
+// and 1537.
+enum class Few { kNo, kCopy2, kCopy4, kSwap16, kSwap32 };
+Few few_rows(int64_t M, int64_t tiles_n) {
+    if (M > 64 || tiles_n > sm_count()) return Few::kNo;
+    const bool shared = 2 * tiles_n <= sm_count();
+    if (M > 32) return shared ? Few::kCopy2 : Few::kNo;
+    return shared ? Few::kCopy4 : M <= 16 ? Few::kSwap16 : Few::kSwap32;
+}
+
 // clusters of `size` CTAs of the kernel's shape that fit on the device at once
 int split_fit(int size) {
     static std::atomic<int> fit[kMaxSplit + 1][64];
@@ -935,14 +1016,13 @@ template <bool FINE, int OUT>
 cudaError_t launch_gated(const CUtensorMap& ma, const CUtensorMap& mg, const CUtensorMap& mu, GatedParams& p,
                          uint32_t idesc, cudaStream_t s) {
     if constexpr (FINE) {
-        // A fold's time is the latency of its TMEM loads: few rows share them out among all
-        // warps.  Copying A twice only pays where a cluster shares a tile (64 x 2048 x 7168:
-        // 13.5 against 14.0 us; 64 x 18432 x 7168, a tile per SM: 50.2 against 48.6).
-        const bool dup4 = p.M <= 32 && p.tiles_n <= sm_count();
-        if (dup4 || (p.M <= 64 && 2 * p.tiles_n <= sm_count())) {
+        const Few few = few_rows(p.M, p.tiles_n);
+        if (few != Few::kNo) {
             p.split = choose_split(p, 380, true);
-            return dup4 ? launch_gated_mode<FINE, OUT, kDup4>(ma, mg, mu, p, idesc, s)
-                        : launch_gated_mode<FINE, OUT, kDup2>(ma, mg, mu, p, idesc, s);
+            return few == Few::kSwap16 ? launch_gated_mode<FINE, OUT, kFew16>(ma, mg, mu, p, idesc, s)
+                 : few == Few::kSwap32 ? launch_gated_mode<FINE, OUT, kFew32>(ma, mg, mu, p, idesc, s)
+                 : few == Few::kCopy4 ? launch_gated_mode<FINE, OUT, kDup4>(ma, mg, mu, p, idesc, s)
+                                      : launch_gated_mode<FINE, OUT, kDup2>(ma, mg, mu, p, idesc, s);
         }
     }
     p.split = choose_split(p, FINE ? 480 : 330, false);
@@ -988,7 +1068,9 @@ fp8q_status launch_gated_mm(const GatedProblem& g, cudaStream_t s) {
     // when the tiles give two CTAs each to nine tenths of the SMs
     const int64_t tall_tiles = ((M + 2 * BM - 1) / (2 * BM)) * ((I + kHN - 1) / kHN);
     const bool pairs = !g.fine && M >= 2 * BM && tall_tiles * 20 >= 9LL * sm_count();
-    // fewer than 128 rows: only they (rounded up to 16) are loaded, see scaled_mm.cu
+    // fewer than 128 rows: only they (rounded up to 16, a valid N of swapped operands) are loaded
+    const Few few = g.fine ? few_rows(M, (I + kHN - 1) / kHN) : Few::kNo;
+    const bool swapped = few == Few::kSwap16 || few == Few::kSwap32;
     const int a_rows = M >= BM ? BM : static_cast<int>((M + 15) / 16 * 16);
     CUtensorMap ma, mg, mu;
     memset(&ma, 0, sizeof(ma));
@@ -1035,7 +1117,7 @@ fp8q_status launch_gated_mm(const GatedProblem& g, cudaStream_t s) {
                          : launch_gated_pair<kBF16>(ma, mg, mu, p, idesc, s);
         return cuda_status(e);
     }
-    const uint32_t idesc = instr_desc(g.fa, g.fb, kBN);
+    const uint32_t idesc = swapped ? instr_desc(g.fb, g.fa, a_rows) : instr_desc(g.fa, g.fb, kBN);
     if (g.q) e = launch_gated<true, kOutQuant>(ma, mg, mu, p, idesc, s);
     else if (g.fine)
         e = g.yt == kF32 ? launch_gated<true, kF32>(ma, mg, mu, p, idesc, s)

@@ -133,12 +133,13 @@ def check_tensor(fp8q, M, I, K, yt, act="silu", fa=E4, fb=E4, with_gu=True, offs
     assert torch.equal(again, out.t)
 
 
-# the same at the borders between the kernel's forms: at most 32 and 64 rows (all rows in every
-# warp's TMEM lanes) with a cluster for a tile and with a tile for each CTA, and persistent tiles
+# the same at the borders between the kernel's forms: at most 16, 32 and 64 rows with a cluster for a
+# tile (copies of the rows) and with a tile for each CTA (operands swapped), and persistent tiles
 # whose rows are no multiples of 32 bytes (words, bytes), of 16 and of an element
 @pytest.mark.parametrize("M,I,K", [(16, 2048, 1024), (17, 2048, 1024), (32, 18000, 256), (33, 9000, 256), (64, 1536, 640),
                                    (64, 18432, 128), (65, 9500, 128), (3, 18944, 128), (2, 19000, 128), (30, 19072, 256),
-                                   (300, 8972, 256), (300, 9001, 128), (300, 8976, 128), (140, 19001, 48)])
+                                   (300, 8972, 256), (300, 9001, 128), (300, 8976, 128), (140, 19001, 48),
+                                   (1, 9600, 1040), (16, 10000, 640), (17, 9601, 2000), (31, 9473, 16), (9, 9472, 0)])
 def test_blockwise_forms(fp8q, M, I, K):
     check_quant(fp8q, M, I, K)
     for yt in (BF16, F32):
