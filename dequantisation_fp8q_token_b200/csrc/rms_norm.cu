@@ -264,6 +264,54 @@ rms_norm_vec_kernel(const FwdParams p) {
     }
 }
 
+// Forward to y for widths and pointers that no vector fits, up to 8192
+// columns: the vector kernel's plan with single elements (element k of thread
+// t is k * blockDim.x + t), so a row is still read once and a thread's loads
+// are in flight together.  Bound by the load and store instructions: bf16
+// 16384 x 1001 with a residual 45.8 us (the generic kernel 111.7), 4096 x 7169
+// 122 (159), 16384 x 100 without one 6.7 (29.4).
+template <int XT, int WT, int K>
+__global__ void __launch_bounds__(512)
+rms_norm_elem_kernel(const FwdParams p) {
+    constexpr int ES = ElemBytes<XT>::value, WS = ElemBytes<WT>::value;
+    __shared__ float sh[32 * 8];
+    pdl_begin();
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+    const bool live = row < p.m;
+    const int64_t base = (live ? row : p.m - 1) * p.n;
+    const int last = static_cast<int>(p.n) - 1, tpr = blockDim.x;
+    float f[K];
+    // every load unconditional, so that all are in flight: past the end, the last element again
+#pragma unroll
+    for (int k = 0; k < K; ++k) f[k] = elem_load<XT>(p.x + (base + min(static_cast<int>(threadIdx.x) + k * tpr, last)) * ES);
+    if (p.res) {
+        float g[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            g[k] = elem_load<XT>(p.res + (base + min(static_cast<int>(threadIdx.x) + k * tpr, last)) * ES);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int c = threadIdx.x + k * tpr;
+            f[k] = round_to<XT>(__fadd_rn(f[k], g[k]));
+            if (live && c <= last) elem_store<XT>(p.res_out + (base + c) * ES, f[k]);
+        }
+    }
+    float s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        f[k] = static_cast<int>(threadIdx.x) + k * tpr <= last ? f[k] : 0.0f;
+        s = __fmaf_rn(f[k], f[k], s);
+    }
+    const float rstd = rstd_of(row_sum(s, sh), p.inv_n, p.eps);
+    if (live && p.rstd && threadIdx.x == 0) p.rstd[row] = rstd;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int c = threadIdx.x + k * tpr;
+        f[k] = __fmul_rn(__fmul_rn(f[k], rstd), elem_load<WT>(p.w + min(c, last) * WS));
+        if (live && c <= last) elem_store<XT>(p.y + (base + c) * ES, f[k]);
+    }
+}
+
 // Forward for every other layout (any width, any group that divides it,
 // element-aligned pointers, rows too long for registers): one CTA per row,
 // which reads the row again (from L2) for each of the three steps.  The sum
@@ -566,6 +614,51 @@ rms_norm_dw_generic_kernel(const float* __restrict__ part, int parts, int64_t n,
     }
 }
 
+// Backward, dx, for widths and pointers that no vector fits, up to 4096
+// columns: as the forward's, one element at a time, dy and r read once (bf16
+// 16384 x 1001 48.3 us, the generic kernel 67.1; with 16 elements a thread
+// 4096 x 7169 took 107.7 and takes 103.8 there).
+template <int XT, int WT, int K>
+__global__ void __launch_bounds__(512)
+rms_norm_bwd_elem_kernel(const BwdParams p) {
+    constexpr int ES = ElemBytes<XT>::value, WS = ElemBytes<WT>::value;
+    __shared__ float sh[32 * 8];
+    pdl_begin();
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+    const bool live = row < p.m;
+    const int64_t base = (live ? row : p.m - 1) * p.n;
+    const int last = static_cast<int>(p.n) - 1, tpr = blockDim.x;
+    const float rstd = __ldg(p.rstd + (live ? row : p.m - 1));
+    float t[K], x[K], d[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int64_t e = base + min(static_cast<int>(threadIdx.x) + k * tpr, last);
+        t[k] = elem_load<XT>(p.dy + e * ES);
+        x[k] = elem_load<XT>(p.r + e * ES);
+        d[k] = 0.0f;
+    }
+    if (p.dres) {
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            d[k] = elem_load<XT>(p.dres + (base + min(static_cast<int>(threadIdx.x) + k * tpr, last)) * ES);
+    }
+    float s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int c = threadIdx.x + k * tpr;
+        t[k] = __fmul_rn(t[k], elem_load<WT>(p.w + min(c, last) * WS));
+        x[k] = __fmul_rn(x[k], rstd);
+        if (c <= last) s = __fmaf_rn(t[k], x[k], s);
+    }
+    const float mean = __fmul_rn(row_sum(s, sh), p.inv_n);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int c = threadIdx.x + k * tpr;
+        const float o = __fadd_rn(__fmul_rn(rstd, __fmaf_rn(-x[k], mean, t[k])), d[k]);
+        if (live && c <= last) elem_store<XT>(p.dx + (base + c) * ES, o);
+    }
+}
+
 // Backward for every other layout: one CTA per row for dx ...
 template <int XT, int WT>
 __global__ void __launch_bounds__(256)
@@ -766,6 +859,13 @@ fp8q_status run_fwd(const FwdParams& p0, cudaStream_t s) {
         }
         if (ok) vb = b;
     }
+    if (!vb && !p.q && p.n <= 8192) {
+        const int k = p.n <= 4096 ? 8 : 16;
+        const int tpr = round32((p.n + k - 1) / k), rows = tpr >= 256 ? 1 : 256 / tpr < 8 ? 256 / tpr : 8;
+        const dim3 grid(static_cast<unsigned>((p.m + rows - 1) / rows)), block(tpr, rows);
+        return cuda_status(k == 8 ? launch_kernel(rms_norm_elem_kernel<XT, WT, 8>, grid, block, s, p)
+                                  : launch_kernel(rms_norm_elem_kernel<XT, WT, 16>, grid, block, s, p));
+    }
     if (!vb) {
         const int64_t cap = static_cast<int64_t>(sm_count()) * 8;
         return cuda_status(launch_kernel(rms_norm_generic_kernel<XT, WT>,
@@ -864,8 +964,15 @@ fp8q_status run_bwd(const BwdParams& p, void* dw, cudaStream_t s) {
         else st = run_bwd_vec<XT, WT, KMAX>(p, &parts, s);
     } else {
         const int64_t cap = static_cast<int64_t>(sm_count()) * 8;
-        st = cuda_status(launch_kernel(rms_norm_bwd_dx_kernel<XT, WT>,
-                                       dim3(static_cast<unsigned>(p.m < cap ? p.m : cap)), dim3(256), s, p));
+        if (p.n <= 4096) {
+            constexpr int k = 8;
+            const int tpr = round32((p.n + k - 1) / k), rows = tpr >= 256 ? 1 : 256 / tpr < 8 ? 256 / tpr : 8;
+            const dim3 grid(static_cast<unsigned>((p.m + rows - 1) / rows)), block(tpr, rows);
+            st = cuda_status(launch_kernel(rms_norm_bwd_elem_kernel<XT, WT, k>, grid, block, s, p));
+        } else {
+            st = cuda_status(launch_kernel(rms_norm_bwd_dx_kernel<XT, WT>,
+                                           dim3(static_cast<unsigned>(p.m < cap ? p.m : cap)), dim3(256), s, p));
+        }
         if (st == FP8Q_OK && p.part) {
             const int64_t want = bwd_parts(p.m), per = (p.m + want - 1) / want;
             parts = (p.m + per - 1) / per;

@@ -293,3 +293,24 @@ def test_forward_many_wide_rows(fp8q, m, n, group):
     for dt, res in ((BF16, True), (F16, False), (F32, True)):
         x, r, w = make(m, n, dt, res)
         check_forward(fp8q, x, r, w, group)
+
+
+# widths and pointers that no vector fits: single elements in registers up to 8192 columns forward
+# and 4096 backward, element by element from memory above
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("res", [False, True])
+@pytest.mark.parametrize("m,n", [(700, 1001), (520, 100), (530, 4095), (513, 4097), (515, 8191), (3, 8193), (1, 1), (600, 2)])
+def test_odd_widths(fp8q, dt, res, m, n):
+    x, r, w = make(m, n, dt, res)
+    y, rstd = Guarded(m * n, dt), Guarded(m, F32)
+    out = Guarded(m * n, dt) if res else None
+    fp8q.fp8q_rms_norm_quant(x, w, y=y.t, residual=r, residual_out=out.t.view(m, n) if res else None, rstd=rstd.t, eps=EPS)
+    for g in (y, rstd, out):
+        if g is not None:
+            g.check()
+    r64, rstd64, v = P.norm(x, w, r, EPS)
+    assert ((rstd.t.double() - rstd64.view(-1)).abs() <= rel(n) * rstd64.view(-1)).all()
+    assert ((y.t.view(m, n).double() - v).abs() <= v.abs() * (rel(n) + P.half_step(dt)) + P.tiny(dt)).all()
+    if res:
+        assert torch.equal(out.t.view(m, n).double(), r64)
+    check_backward(fp8q, m, n, dt, res)
