@@ -684,21 +684,32 @@ rms_norm_bwd_dx_kernel(const BwdParams p) {
         }
     }
 }
-// ... and 256 columns x one slice of the rows per CTA for the partial sums of dw
-template <int XT>
+// ... and COLS columns x one slice of the rows per CTA, 256 / COLS rows at a
+// time, for the partial sums of dw: 256 columns, or 32 where that leaves most
+// of the threads without one (bf16 16384 x 100: 13.9 us with dx, 22.2 with 256;
+// 4096 x 7169: 176 and 148)
+template <int XT, int COLS>
 __global__ void __launch_bounds__(256)
 rms_norm_bwd_part_kernel(const BwdParams p, int64_t rows_per_part) {
     constexpr int ES = ElemBytes<XT>::value;
+    constexpr int ROWS = 256 / COLS;
+    __shared__ float sh[ROWS][COLS + 1];
     pdl_begin();
-    const int64_t c = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (c >= p.n) return;
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * COLS + threadIdx.x;
     const int64_t r0 = static_cast<int64_t>(blockIdx.y) * rows_per_part;
     const int64_t r1 = r0 + rows_per_part < p.m ? r0 + rows_per_part : p.m;
     float s = 0.0f;
-    for (int64_t row = r0; row < r1; ++row)
-        s = __fmaf_rn(elem_load<XT>(p.dy + (row * p.n + c) * ES),
-                      __fmul_rn(elem_load<XT>(p.r + (row * p.n + c) * ES), __ldg(p.rstd + row)), s);
-    p.part[static_cast<int64_t>(blockIdx.y) * p.n + c] = s;
+    if (c < p.n) {
+        for (int64_t row = r0 + threadIdx.y; row < r1; row += ROWS)
+            s = __fmaf_rn(elem_load<XT>(p.dy + (row * p.n + c) * ES),
+                          __fmul_rn(elem_load<XT>(p.r + (row * p.n + c) * ES), __ldg(p.rstd + row)), s);
+    }
+    sh[threadIdx.y][threadIdx.x] = s;
+    __syncthreads();
+    if (threadIdx.y == 0 && c < p.n) {
+        for (int i = 1; i < ROWS; ++i) s += sh[i][threadIdx.x];
+        p.part[static_cast<int64_t>(blockIdx.y) * p.n + c] = s;
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -974,11 +985,13 @@ fp8q_status run_bwd(const BwdParams& p, void* dw, cudaStream_t s) {
                                            dim3(static_cast<unsigned>(p.m < cap ? p.m : cap)), dim3(256), s, p));
         }
         if (st == FP8Q_OK && p.part) {
+            const int cols = p.n <= 512 ? 32 : 256;
             const int64_t want = bwd_parts(p.m), per = (p.m + want - 1) / want;
             parts = (p.m + per - 1) / per;
-            st = cuda_status(launch_kernel(rms_norm_bwd_part_kernel<XT>,
-                                           dim3(static_cast<unsigned>((p.n + 255) / 256), static_cast<unsigned>(parts)),
-                                           dim3(256), s, p, per));
+            const dim3 grid(static_cast<unsigned>((p.n + cols - 1) / cols), static_cast<unsigned>(parts));
+            st = cuda_status(cols == 32
+                                 ? launch_kernel(rms_norm_bwd_part_kernel<XT, 32>, grid, dim3(32, 8), s, p, per)
+                                 : launch_kernel(rms_norm_bwd_part_kernel<XT, 256>, grid, dim3(256), s, p, per));
         }
     }
     if (st != FP8Q_OK || !dw) return st;
