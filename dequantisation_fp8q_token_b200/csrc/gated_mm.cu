@@ -35,6 +35,7 @@
 //     CTA pairs (tcgen05.mma.cta_group::2), the even CTA loading the tile's
 //     rows of Wg and the odd one its rows of Wu.
 #include <cstring>
+#include <type_traits>
 
 #include "gated_device.cuh"
 #include "mm_device.cuh"
@@ -559,20 +560,33 @@ gated_mm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
                     // are aligned, else 16 bytes at a time
                     uint32_t* area = reinterpret_cast<uint32_t*>(stage_area);
                     __syncwarp();
+                    auto stage_words = [&](auto e4m3) {
 #pragma unroll
-                    for (int i = 0; i < kHalf / 4; ++i)
-                        asm volatile("st.shared.b32 [%0], %1;" :: "r"(smem_u32(area + lane * kStagePitch + i)), "r"(word(i)) : "memory");
+                        for (int i = 0; i < kHalf / 4; ++i) {
+                            const float a = __fmul_rn(accum[2 * i].x, scale), b = __fmul_rn(accum[2 * i].y, scale);
+                            const float c = __fmul_rn(accum[2 * i + 1].x, scale), d = __fmul_rn(accum[2 * i + 1].y, scale);
+                            const uint32_t w = decltype(e4m3)::value ? enc4<kE4M3>(a, b, c, d) : enc4<kE5M2>(a, b, c, d);
+                            asm volatile("st.shared.b32 [%0], %1;" :: "r"(smem_u32(area + lane * kStagePitch + i)), "r"(w) : "memory");
+                        }
+                    };
+                    if (p.fmt == kE4M3) stage_words(std::true_type());
+                    else stage_words(std::false_type());
                     __syncwarp();
-                    const int l = lane & 15;
-                    for (int r = lane >> 4; r < 32 && row - lane + r < p.M; r += 2) {
-                        uint8_t* qrow = p.q + static_cast<int64_t>(row - lane + r) * p.I + col0;
-                        if (p.align_q >= 4) {
-                            if (col0 + 4 * l < p.I) st_u32(qrow + 4 * l, area[r * kStagePitch + l]);
-                        } else {
+                    const int l = lane & 15, rows = p.M - (row - lane);       // of this warp
+                    uint8_t* q0 = p.q + static_cast<int64_t>(row - lane) * p.I + col0;
+                    if (p.align_q >= 4) {
+#pragma unroll 8
+                        for (int r = lane >> 4; r < 32; r += 2) {
+                            const uint32_t w = area[r * kStagePitch + l];
+                            if (r < rows && col0 + 4 * l < p.I) st_u32(q0 + static_cast<int64_t>(r) * p.I + 4 * l, w);
+                        }
+                    } else {
+#pragma unroll 2
+                        for (int r = lane >> 4; r < 32; r += 2) {
                             const uint8_t* codes = reinterpret_cast<const uint8_t*>(area + r * kStagePitch);
 #pragma unroll
-                            for (int c = l; c < kHalf; c += 16)
-                                if (col0 + c < p.I) qrow[c] = codes[c];
+                            for (int c = 0; c < kHalf; c += 16)
+                                if (r < rows && col0 + c + l < p.I) q0[static_cast<int64_t>(r) * p.I + c + l] = codes[c + l];
                         }
                     }
                 }
