@@ -38,7 +38,11 @@ def _native():
     global _ops
     if _ops is None:
         lib()
-        from . import _fp8q_torch
+        try:
+            from . import _fp8q_torch
+        except ImportError as e:
+            raise ImportError("_fp8q_torch.so is missing or was built against another torch; build it with "
+                              "`python -m dequantisation_fp8q_token_b200.build` (needs g++)") from e
         _ops = _fp8q_torch
     return _ops
 

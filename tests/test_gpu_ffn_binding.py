@@ -208,3 +208,84 @@ def test_training_steps_in_graphs(fp8q):
         got = [t.clone() for t in out]
         for a, b in zip(got, step()):
             assert torch.equal(a, b)
+
+
+def test_any_one_input_may_ask_for_its_gradient(fp8q):
+    """The gradient of one input alone has the bits that it has beside the others'."""
+    x, r, w = rand(700, 256), rand(700, 256, seed=1), rand(256, seed=2)
+    dy, dr = rand(700, 256, seed=3), rand(700, 256, seed=4)
+    wide = rand(64, 256, seed=5)
+    dh = rand(700, 32, seed=6)
+
+    def norm_grads(which):
+        t = [v.clone().requires_grad_(i in which) for i, v in enumerate((x, r, w))]
+        out = fp8q.rms_norm(t[0], t[2], residual=t[1])
+        return torch.autograd.grad(out, [t[i] for i in which], (dy, dr))
+
+    every = norm_grads((0, 1, 2))
+    for i in range(3):
+        assert torch.equal(norm_grads((i,))[0], every[i])
+
+    def gated_grads(which):
+        t = [v.clone().requires_grad_(i in which) for i, v in enumerate((x, wide))]
+        return torch.autograd.grad(fp8q.gated_linear_fp8(*t), [t[i] for i in which], dh)
+
+    every = gated_grads((0, 1))
+    for i in range(2):
+        assert torch.equal(gated_grads((i,))[0], every[i])
+    # a gradient that is no memory of its own: expanded from one number
+    a, b = x.clone().requires_grad_(True), x.clone().requires_grad_(True)
+    fp8q.rms_norm(a, w).sum().backward()
+    fp8q.rms_norm(b, w).backward(torch.ones_like(b))
+    assert torch.equal(a.grad, b.grad)
+
+
+def test_threads_on_streams_of_their_own(fp8q):
+    """Four threads at once, each on its stream: every result has the bits of the call alone."""
+    import threading
+    x, w, wide = rand(600, 1024), rand(1024, seed=1), rand(512, 1024, seed=2)
+    ops = fine(40, 2048, 1024)
+
+    def work():
+        a, b, c = (t.clone().requires_grad_(True) for t in (x, w, wide))
+        y = fp8q.rms_norm(a, b)
+        h = fp8q.gated_linear_fp8(y, c)
+        grads = torch.autograd.grad(h, (a, b, c), torch.ones_like(h))
+        q, s = torch.empty(40, 2048, dtype=torch.uint8, device="cuda"), torch.empty(40, 16, device="cuda")
+        fp8q.fp8q_gated_mm_blockwise_quant(*ops, q, s)
+        return [y.detach(), h.detach(), *grads, q, s]
+
+    want = work()
+    torch.cuda.synchronize()
+    got, errors = [None] * 4, []
+
+    def run(i):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                for _ in range(5):
+                    got[i] = work()
+            stream.synchronize()
+        except Exception as e:                      # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+    for g in got:
+        for a, b in zip(g, want):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("M", [0, 1, 3])
+def test_blocks_of_few_tokens(fp8q, M):
+    x = rand(M, 256)
+    _, _, wg, sg, wu, su = fine(1, 128, 256)
+    wd, sd = rand(256, 128, seed=7).to(torch.float8_e4m3fn), torch.ones(2, 1, device="cuda")
+    out, r = fp8q.ffn_fp8_blockwise(x, wg, sg, wu, su, wd, sd, norm_weight=rand(256), residual=x)
+    assert out.shape == r.shape == (M, 256) and out.isfinite().all() and torch.equal(r, x + x)
+    assert fp8q.ffn_fp8_blockwise(x, wg, sg, wu, su, wd, sd).shape == (M, 256)
+    assert fp8q.gated_linear_fp8_blockwise(x.view(M, 1, 256), wg, sg, wu, su).shape == (M, 1, 128)
