@@ -16,7 +16,7 @@
 // scaled_mm.cu: warp 0 copies (TMA), warp 1 issues the MMAs, warps 2-9 fold,
 // activate and store.
 //
-// Three kernels' worth of shapes:
+// Kernels and their forms:
 //   gated_mm_kernel, persistent   128 x (128 + 128) tiles (kWide; kRagged where
 //     the output's rows are not multiples of 32 bytes);
 //   gated_mm_kernel, kCluster     when the tiles would fill at most half of

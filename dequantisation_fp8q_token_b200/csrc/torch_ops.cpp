@@ -9,6 +9,7 @@
 // a status other than 0 (a RuntimeError with the same text out of a backward
 // pass, which runs on another thread).
 #include <ATen/cuda/CUDAContext.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <torch/csrc/autograd/functions/basic_ops.h>
 #include <torch/extension.h>
 
@@ -110,6 +111,11 @@ fp8q_stream_t on_device(const Tensor& x, const Others&... others) {
     return stream_of(x);
 }
 
+// memory on x's device, from the caching allocator without a turn through the dispatcher
+Tensor empty(at::IntArrayRef sizes, at::ScalarType dtype, const Tensor& x) {
+    return Tensor(at::detail::empty_cuda(sizes, dtype, x.device(), std::nullopt));
+}
+
 std::string shape_of(const Tensor& t) {
     return text(t.sizes());
 }
@@ -185,10 +191,10 @@ struct RmsNorm : torch::autograd::Function<RmsNorm> {
         const Tensor x = x_in.contiguous(), weight = weight_in.contiguous();
         const auto [m, n] = rows_of(x, weight);
         const fp8q_dtype xt = dtype_code(x, "x"), wt = dtype_code(weight, "weight");
-        Tensor y = at::empty_like(x), rstd = at::empty({m}, x.options().dtype(at::kFloat)), residual, r;
+        Tensor y = empty(x.sizes(), x.scalar_type(), x), rstd = empty({m}, at::kFloat, x), residual, r;
         if (residual_in) {
             residual = residual_in->contiguous();
-            r = at::empty_like(x);
+            r = empty(x.sizes(), x.scalar_type(), x);
         }
         check(fp8q_rms_norm_quant(x.data_ptr(), xt, r.defined() ? residual.data_ptr() : nullptr,
                                   r.defined() ? r.data_ptr() : nullptr, weight.data_ptr(), wt, m, n,
@@ -197,12 +203,11 @@ struct RmsNorm : torch::autograd::Function<RmsNorm> {
               "fp8q_rms_norm_quant");
         ctx->set_materialize_grads(false);
         ctx->save_for_backward({r.defined() ? r : x, weight, rstd});
-        ctx->saved_data["has_residual"] = r.defined();
         return r.defined() ? variable_list{y, r} : variable_list{y};
     }
 
     static variable_list backward(AutogradContext* ctx, variable_list grads) {
-        const bool graph = at::GradMode::is_enabled(), has_residual = ctx->saved_data["has_residual"].toBool();
+        const bool graph = at::GradMode::is_enabled(), has_residual = grads.size() == 2;
         at::AutoGradMode off(false);
         const Tensor dr_in = has_residual ? grads[1] : Tensor();
         if (!grads[0].defined())                    // only the sum was used: its gradient as it is
@@ -212,13 +217,13 @@ struct RmsNorm : torch::autograd::Function<RmsNorm> {
         const fp8q_stream_t st = on_device(r, grads[0], dr_in);
         const Tensor dy = grads[0].contiguous(), dr = dr_in.defined() ? dr_in.contiguous() : Tensor();
         const auto [m, n] = rows_of(r, weight);
-        Tensor dx = at::empty_like(r), dw, workspace;
+        Tensor dx = empty(r.sizes(), r.scalar_type(), r), dw, workspace;
         size_t bytes = 0;
         if (ctx->needs_input_grad(1)) {
-            dw = at::empty_like(weight);
+            dw = empty(weight.sizes(), weight.scalar_type(), r);
             // a workspace of this call's own: the caching allocator orders it by stream and by graph
             bytes = fp8q_rms_norm_bwd_workspace_bytes(m, n);
-            if (bytes) workspace = at::empty({static_cast<int64_t>(bytes)}, r.options().dtype(at::kByte));
+            if (bytes) workspace = empty({static_cast<int64_t>(bytes)}, at::kByte, r);
         }
         check(fp8q_rms_norm_bwd(dy.data_ptr(), r.data_ptr(), dtype_code(r, "x"), weight.data_ptr(),
                                 dtype_code(weight, "weight"), rstd.data_ptr<float>(), dr.defined() ? dr.data_ptr() : nullptr,
@@ -355,9 +360,9 @@ struct GatedLinear : torch::autograd::Function<GatedLinear> {
         const int64_t I = w.size(0) / 2, K = w.size(1), T = rows_before_last(x.sizes());
         std::vector<int64_t> shape = x.sizes().vec();
         shape.back() = I;
-        Tensor h = at::empty(shape, x.options());
+        Tensor h = empty(shape, x.scalar_type(), x);
         const Parts<6> at_ = parts(T, I, K, x.element_size(), keep);
-        const Tensor buf = at::empty({at_.bytes}, x.options().dtype(at::kByte));
+        const Tensor buf = empty({at_.bytes}, at::kByte, x);
         uint8_t* b = static_cast<uint8_t*>(buf.data_ptr());
         uint8_t *x8 = b + at_.at[0], *w8 = b + at_.at[1];
         auto *sx = reinterpret_cast<float*>(b + at_.at[2]), *sw = reinterpret_cast<float*>(b + at_.at[3]);
@@ -369,9 +374,7 @@ struct GatedLinear : torch::autograd::Function<GatedLinear> {
               "fp8q_gated_mm");
         if (keep) {
             ctx->save_for_backward({buf});
-            ctx->saved_data["act"] = act;
-            ctx->saved_data["x_shape"] = x.sizes().vec();
-            ctx->saved_data["w_shape"] = w.sizes().vec();
+            ctx->saved_data["k_act"] = 2 * K + act;           // the other sizes are the gradient's
         }
         return {h};
     }
@@ -382,18 +385,16 @@ struct GatedLinear : torch::autograd::Function<GatedLinear> {
         const Tensor buf = ctx->get_saved_variables()[0];
         const fp8q_stream_t st = on_device(buf, grads[0]);
         const Tensor dh = grads[0].contiguous();
-        const auto act = static_cast<fp8q_activation>(ctx->saved_data["act"].toInt());
-        const std::vector<int64_t> x_shape = ctx->saved_data["x_shape"].toIntVector();
-        const std::vector<int64_t> w_shape = ctx->saved_data["w_shape"].toIntVector();
-        const int64_t I = w_shape[0] / 2, K = w_shape[1];
-        const int64_t T = rows_before_last(x_shape);
+        const int64_t k_act = ctx->saved_data["k_act"].toInt(), K = k_act / 2;
+        const auto act = static_cast<fp8q_activation>(k_act % 2);
+        const int64_t I = dh.size(-1), T = rows_before_last(dh.sizes());
         const Parts<6> at_ = parts(T, I, K, dh.element_size(), true);
         uint8_t* b = static_cast<uint8_t*>(buf.data_ptr());
         const uint8_t *x8 = b + at_.at[0], *w8 = b + at_.at[1];
         const auto *sx = reinterpret_cast<const float*>(b + at_.at[2]), *sw = reinterpret_cast<const float*>(b + at_.at[3]);
         const fp8q_dtype dt = dtype_code(dh, "the gradient");
         const Parts<3> to({2 * T * I, 4, static_cast<int64_t>(cast_workspace())});
-        const Tensor tmp = at::empty({to.bytes}, buf.options());
+        const Tensor tmp = empty({to.bytes}, at::kByte, buf);
         uint8_t* d8 = static_cast<uint8_t*>(tmp.data_ptr());
         float* sd = reinterpret_cast<float*>(d8 + to.at[1]);
         check(fp8q_gated_bwd_cast(dh.data_ptr(), b + at_.at[5], dt, T, I, act, FP8Q_E5M2, d8, sd, d8 + to.at[2],
@@ -402,14 +403,16 @@ struct GatedLinear : torch::autograd::Function<GatedLinear> {
         Tensor dx, dw;
         if (ctx->needs_input_grad(0)) {
             // dx[T, K] = d[T, 2 I] @ w[2 I, K], one product over gate's and up's columns together
-            dx = at::empty(x_shape, dh.options());
+            std::vector<int64_t> shape = dh.sizes().vec();
+            shape.back() = K;
+            dx = empty(shape, dh.scalar_type(), buf);
             check(fp8q_scaled_mm_ex(d8, FP8Q_E5M2, FP8Q_K_MAJOR, w8, FP8Q_E4M3FN, FP8Q_MN_MAJOR, T, K, 2 * I, sd, sw, nullptr,
                                     dt, dx.data_ptr(), nullptr, st),
                   "fp8q_scaled_mm_ex");
         }
         if (ctx->needs_input_grad(1)) {
             // dw[2 I, K] = d^T[2 I, T] @ x[T, K], any token count
-            dw = at::empty(w_shape, dh.options());
+            dw = empty({2 * I, K}, dh.scalar_type(), buf);
             check(fp8q_scaled_mm_ex(d8, FP8Q_E5M2, FP8Q_MN_MAJOR, x8, FP8Q_E4M3FN, FP8Q_MN_MAJOR, 2 * I, K, T, sd, sx, nullptr,
                                     dt, dw.data_ptr(), nullptr, st),
                   "fp8q_scaled_mm_ex");
