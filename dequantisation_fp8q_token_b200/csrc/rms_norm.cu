@@ -13,6 +13,8 @@
 #include "fp8q_device.cuh"
 #include "fp8q_internal.h"
 
+#include <type_traits>
+
 namespace fp8q {
 namespace {
 
@@ -73,6 +75,24 @@ __device__ __forceinline__ Weights<WT, N> load_weights(const uint8_t* __restrict
     const uint4* src = reinterpret_cast<const uint4*>(w + static_cast<int64_t>(e) * ElemBytes<WT>::value);
 #pragma unroll
     for (int j = 0; j < N * ElemBytes<WT>::value / 16; ++j) r.v[j] = __ldg(src + j);
+    return r;
+}
+// the same from any place and alignment; zeros for elements outside the row's 0 .. n - 1
+template <int WT, int N>
+__device__ __forceinline__ Weights<WT, N> load_weights_any(const uint8_t* __restrict__ w, int e, int n) {
+    using Bits = std::conditional_t<ElemBytes<WT>::value == 4, uint32_t, uint16_t>;
+    Weights<WT, N> r;
+    uint32_t* out = reinterpret_cast<uint32_t*>(r.v);
+    constexpr int PER = 4 / ElemBytes<WT>::value;         // elements of a register
+#pragma unroll
+    for (int j = 0; j < N / PER; ++j) {
+        out[j] = 0u;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int c = e + j * PER + i;
+            if (c >= 0 && c < n) out[j] |= static_cast<uint32_t>(__ldg(reinterpret_cast<const Bits*>(w) + c)) << (16 * i);
+        }
+    }
     return r;
 }
 template <int WT, int N>
@@ -376,6 +396,17 @@ rms_norm_generic_kernel(const FwdParams p) {
 // flight while earlier rows are reduced, and no barrier guards the slots.
 // bf16 4096 x 7168 with a residual: 40.3 us for dx (89% of the measured copy
 // bandwidth), 44.0 with dw.
+// SHIFT, for rows that are no multiple of 16 bytes (and weights anywhere): the
+// tensors' own aligned vectors, so a row starts `off` elements inside its first
+// one.  A thread's vectors lie at the same columns in each of its rows when the
+// rows between them are a multiple of 16 bytes together, which the grid sees
+// to; what a first or last vector holds of the neighbouring rows is set to
+// zero in its slot, and such a vector's dx is stored by elements.  With a
+// residual and dw fp16 4096 x 4001 39.8 us and 1600 x 18001 78.6, bf16 16384 x
+// 1001 41.5, fp32 5060 x 5690 95.6 (73% of the copy bandwidth), against 96.3,
+// 174, 69.6 and 199 with single elements in two passes; bf16 4096 x 7169 82.7
+// (145), where the row's last vector makes a thread hold four (4096 x 7001
+// 58.6).
 // ---------------------------------------------------------------------------
 struct BwdParams {
     const uint8_t* dy;
@@ -393,6 +424,10 @@ struct BwdParams {
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
 }
+// the first `bytes` of the 16, zeros after them
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // wait until at most `pending` of this thread's groups are in flight
 __device__ __forceinline__ void cp_async_wait(int pending) {
@@ -408,6 +443,11 @@ __device__ __forceinline__ Vec<16> ld_shared16(uint32_t a) {
     return v;
 }
 
+template <int BYTES> __device__ __forceinline__ void st_shared_zero(uint32_t a) {
+    if constexpr (BYTES == 4) asm volatile("st.shared.b32 [%0], %1;" :: "r"(a), "r"(0) : "memory");
+    else asm volatile("st.shared.b16 [%0], %1;" :: "r"(a), "h"(static_cast<uint16_t>(0)) : "memory");
+}
+
 constexpr int kBwdMaxStages = 4;
 // Threads of a CTA at most, and registers a thread that its bounds leave: up to
 // 8 elements of a row a thread 512 and 64, up to 16 448 and 72 (two CTAs an
@@ -419,7 +459,7 @@ template <int XT, int K> struct BwdShape {
     static constexpr int kRegs = kElems <= 8 ? 64 : kElems <= 16 ? 72 : 96;
 };
 
-template <int XT, int WT, int K>
+template <int XT, int WT, int K, bool SHIFT>
 __global__ void __launch_bounds__(BwdShape<XT, K>::kThreads, BwdShape<XT, K>::kMinCtas)
 rms_norm_bwd_vec_kernel(const BwdParams p) {
     constexpr int ES = ElemBytes<XT>::value;
@@ -430,27 +470,43 @@ rms_norm_bwd_vec_kernel(const BwdParams p) {
     pdl_wait();
     const int tpr = blockDim.x, rows = blockDim.y;
     const int tid = threadIdx.y * tpr + threadIdx.x;
-    const int nvec = static_cast<int>(p.n / EPV);
     const int streams = p.dres ? 3 : 2;
     const int64_t step = static_cast<int64_t>(gridDim.x) * rows;
     const int64_t first = static_cast<int64_t>(blockIdx.x) * rows + threadIdx.y;
+    const int n = static_cast<int>(p.n);
+    // SHIFT: elements of the row's first vector that are the row's before it;
+    // the same for all of a thread's rows, as step * n is a multiple of EPV
+    const int off = SHIFT ? static_cast<int>(first * n & (EPV - 1)) : 0;
+    const int nvec = SHIFT ? (n + off + EPV - 1) / EPV : n / EPV;
     // rows left for this CTA's first thread row, which has the most
     const int iters = p.m > first - threadIdx.y ? static_cast<int>((p.m - (first - threadIdx.y) + step - 1) / step) : 0;
     const uint32_t slot0 = static_cast<uint32_t>(__cvta_generic_to_shared(slots)) + 16 * tid;
     const uint32_t plane = 16 * tpr * rows;              // one vector of every thread
     // slot (stage, stream, k) of this thread
     auto slot = [&](int stage, int stream, int k) { return slot0 + plane * ((stage * streams + stream) * K + k); };
-    const int64_t at = static_cast<int64_t>(threadIdx.x) * EPV;             // of vector 0 in a row
+    const int at = static_cast<int>(threadIdx.x) * EPV - off;               // of vector 0 in a row
     const int pitch = tpr * EPV;
     bool in_row[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) in_row[k] = static_cast<int>(threadIdx.x + k * tpr) < nvec;
+    // vector k holds elements of another row, or of none
+    auto edge = [&](int k) { return SHIFT && (at + k * pitch < 0 || at + k * pitch + EPV > n); };
+    auto inside = [&](int k, int j) { return at + k * pitch + j >= 0 && at + k * pitch + j < n; };
+    bool edges = false;
+#pragma unroll
+    for (int k = 0; k < K; ++k) edges |= in_row[k] && edge(k);
     auto fetch = [&](int64_t row, int stage) {
         if (row < p.m) {
             const int64_t o = (row * p.n + at) * ES;
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                if (in_row[k]) {
+                if (SHIFT && in_row[k]) {
+                    // the last row's last vector may end past the tensor
+                    const int bytes = row == p.m - 1 && at + k * pitch + EPV > n ? (n - at - k * pitch) * ES : 16;
+                    cp_async16(slot(stage, 0, k), p.dy + o + k * pitch * ES, bytes);
+                    cp_async16(slot(stage, 1, k), p.r + o + k * pitch * ES, bytes);
+                    if (streams == 3) cp_async16(slot(stage, 2, k), p.dres + o + k * pitch * ES, bytes);
+                } else if (in_row[k]) {
                     cp_async16(slot(stage, 0, k), p.dy + o + k * pitch * ES);
                     cp_async16(slot(stage, 1, k), p.r + o + k * pitch * ES);
                     if (streams == 3) cp_async16(slot(stage, 2, k), p.dres + o + k * pitch * ES);
@@ -467,7 +523,8 @@ rms_norm_bwd_vec_kernel(const BwdParams p) {
     for (int k = 0; k < K; ++k) {
 #pragma unroll
         for (int j = 0; j < EPV / 2; ++j) acc[k][j] = both(0.0f);
-        wv[k] = load_weights<WT, EPV>(p.w, in_row[k] ? static_cast<int>(at) + k * pitch : 0);
+        if constexpr (SHIFT) wv[k] = load_weights_any<WT, EPV>(p.w, at + k * pitch, n);
+        else wv[k] = load_weights<WT, EPV>(p.w, in_row[k] ? at + k * pitch : 0);
     }
     int stage = 0;
     int64_t row = first;
@@ -475,6 +532,17 @@ rms_norm_bwd_vec_kernel(const BwdParams p) {
         const bool live = row < p.m;
         const float rstd = live ? __ldg(p.rstd + row) : 0.0f;
         cp_async_wait(p.stages - 1);
+        if (SHIFT && edges) {                  // zeros for what is not the row's
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                if (!in_row[k] || !edge(k)) continue;
+                for (int j = 0; j < EPV; ++j) {
+                    if (inside(k, j)) continue;
+                    st_shared_zero<ES>(slot(stage, 0, k) + j * ES);
+                    st_shared_zero<ES>(slot(stage, 1, k) + j * ES);
+                }
+            }
+        }
         // sum of t * r, t = dy * w: the row's mean of t * xhat over n / rstd
         float2 sum = both(0.0f);
 #pragma unroll
@@ -511,7 +579,16 @@ rms_norm_bwd_vec_kernel(const BwdParams p) {
                     acc[k][j] = __ffma2_rn(dy[j], xhat, acc[k][j]);
                     o[j] = __ffma2_rn(__ffma2_rn(xhat, both(-mean), __fmul2_rn(dy[j], w[j])), both(rstd), o[j]);
                 }
-                store_vec<16>(p.dx + (row * p.n + at + k * pitch) * ES, pack<XT, 16>(o));
+                uint8_t* dx = p.dx + (row * p.n + at + k * pitch) * ES;
+                if (edge(k)) {
+#pragma unroll
+                    for (int j = 0; j < EPV / 2; ++j) {
+                        if (inside(k, 2 * j)) elem_store<XT>(dx + 2 * j * ES, o[j].x);
+                        if (inside(k, 2 * j + 1)) elem_store<XT>(dx + (2 * j + 1) * ES, o[j].y);
+                    }
+                } else {
+                    store_vec<16>(dx, pack<XT, 16>(o));
+                }
             }
         }
         fetch(row + p.stages * step, stage);
@@ -519,6 +596,31 @@ rms_norm_bwd_vec_kernel(const BwdParams p) {
     }
     cp_async_wait(0);
     if (!p.part) return;
+    if constexpr (SHIFT) {
+        // thread rows start at different places: by columns, the threads' sums in row order
+        float* total = reinterpret_cast<float*>(slots);           // [n], free after the barrier
+        for (int y = rows - 1; y >= 0; --y) {
+            __syncthreads();
+            if (threadIdx.y == y) {
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    if (!in_row[k]) continue;
+                    float v[EPV];                                 // the loads first: none waits for a store
+#pragma unroll
+                    for (int j = 0; j < EPV; ++j)
+                        v[j] = y < rows - 1 ? total[max(0, min(at + k * pitch + j, n - 1))] : 0.0f;
+#pragma unroll
+                    for (int j = 0; j < EPV; ++j) {
+                        const float a = j & 1 ? acc[k][j / 2].y : acc[k][j / 2].x;
+                        if (inside(k, j)) total[at + k * pitch + j] = __fadd_rn(a, v[j]);
+                    }
+                }
+            }
+        }
+        __syncthreads();
+        for (int c = tid; c < n; c += tpr * rows) p.part[static_cast<int64_t>(blockIdx.x) * n + c] = total[c];
+        return;
+    }
     // the CTA's rows of accumulators, added in row order through shared memory
     if (rows > 1) {
         float2* total = reinterpret_cast<float2*>(slots);     // [nvec * EPV / 2], free now
@@ -597,15 +699,25 @@ rms_norm_dw_kernel(const float* __restrict__ part, int parts, int64_t n, uint8_t
         for (int j = 0; j < 4; ++j) elem_store<WT>(dw + (c + j) * ElemBytes<WT>::value, v[j]);
     }
 }
+constexpr int kDwSingles = 10;
 template <int WT>
 __global__ void __launch_bounds__(512)
-rms_norm_dw_generic_kernel(const float* __restrict__ part, int parts, int64_t n, uint8_t* __restrict__ dw) {
+rms_norm_dw_generic_kernel(const float* part, int parts, int64_t n, uint8_t* __restrict__ dw) {
     pdl_begin();
     __shared__ float sh[16][33];
     const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x;
     float s = 0.0f;
-    if (c < n)
-        for (int i = threadIdx.y; i < parts; i += 16) s += part[static_cast<int64_t>(i) * n + c];
+    if (c < n) {
+        for (int i0 = threadIdx.y; i0 < parts; i0 += 16 * kDwSingles) {
+            float v[kDwSingles];
+#pragma unroll
+            for (int j = 0; j < kDwSingles; ++j)                // all in flight: past the end, the last again
+                v[j] = part[static_cast<int64_t>(min(i0 + 16 * j, parts - 1)) * n + c];
+#pragma unroll
+            for (int j = 0; j < kDwSingles; ++j)
+                if (i0 + 16 * j < parts) s += v[j];
+        }
+    }
     sh[threadIdx.y][threadIdx.x] = s;
     __syncthreads();
     if (threadIdx.y == 0 && c < n) {
@@ -614,7 +726,7 @@ rms_norm_dw_generic_kernel(const float* __restrict__ part, int parts, int64_t n,
     }
 }
 
-// Backward, dx, for widths and pointers that no vector fits, up to 4096
+// Backward, dx, for tensors that are not at 16-byte addresses, up to 4096
 // columns: as the forward's, one element at a time, dy and r read once (bf16
 // 16384 x 1001 48.3 us, the generic kernel 67.1; with 16 elements a thread
 // 4096 x 7169 took 107.7 and takes 103.8 there).
@@ -917,11 +1029,10 @@ fp8q_status run_dw(const float* part, int64_t parts, int64_t n, void* dw, cudaSt
 
 constexpr int kSmemPerSm = 222 * 1024;     // dynamic shared memory that CTAs of one SM may share here
 
-template <int XT, int WT, int K>
-fp8q_status run_bwd_vec(const BwdParams& p0, int64_t* parts, cudaStream_t s) {
+template <int XT, int WT, int K, bool SHIFT>
+fp8q_status run_bwd_vec(const BwdParams& p0, int64_t nvec, int64_t* parts, cudaStream_t s) {
     constexpr int EPV = 16 / ElemBytes<XT>::value;
     BwdParams p = p0;
-    const int64_t nvec = p.n / EPV;
     const int tpr = round32((nvec + K - 1) / K);
     using Shape = BwdShape<XT, K>;
     const int rows = Shape::kThreads / tpr;
@@ -931,13 +1042,28 @@ fp8q_status run_bwd_vec(const BwdParams& p0, int64_t* parts, cudaStream_t s) {
     const int per_cta = kSmemPerSm / ctas;
     p.stages = per_cta / stage < kBwdMaxStages ? per_cta / stage : kBwdMaxStages;
     const int smem = p.stages * stage;
-    auto kernel = rms_norm_bwd_vec_kernel<XT, WT, K>;
+    auto kernel = rms_norm_bwd_vec_kernel<XT, WT, K, SHIFT>;
     static std::atomic<bool> allowed[64];
     const cudaError_t e = allow_smem(kernel, kSmemPerSm, allowed);
     if (e != cudaSuccess) return cuda_status(e);
     const int64_t cap = static_cast<int64_t>(ctas) * sm_count(), want = (p.m + rows - 1) / rows;
     *parts = want < cap ? want : cap;
+    if (SHIFT && want > cap) {          // several turns: each moves a thread by a multiple of EPV elements
+        int64_t turn = EPV;
+        while (turn > 1 && (turn / 2) * rows * p.n % EPV == 0) turn /= 2;
+        if (cap < turn) return FP8Q_ERR_CUDA;      // not reached: every such GPU has more SMs
+        *parts = cap - cap % turn;
+    }
     return cuda_status(launch_kernel_smem(kernel, dim3(static_cast<unsigned>(*parts)), dim3(tpr, rows), smem, s, p));
+}
+
+template <int XT, int WT, bool SHIFT>
+fp8q_status run_bwd_vec_k(const BwdParams& p, int64_t nvec, int64_t* parts, cudaStream_t s) {
+    constexpr int KMAX = 2 * ElemBytes<XT>::value;         // 32 elements of a row per thread at most
+    if (nvec <= BwdShape<XT, 1>::kThreads) return run_bwd_vec<XT, WT, 1, SHIFT>(p, nvec, parts, s);
+    if (nvec <= 2 * BwdShape<XT, 2>::kThreads) return run_bwd_vec<XT, WT, 2, SHIFT>(p, nvec, parts, s);
+    if (KMAX == 4 || nvec <= 4 * BwdShape<XT, 4>::kThreads) return run_bwd_vec<XT, WT, 4, SHIFT>(p, nvec, parts, s);
+    return run_bwd_vec<XT, WT, KMAX, SHIFT>(p, nvec, parts, s);
 }
 
 template <int XT, int WT, int V>
@@ -955,13 +1081,15 @@ fp8q_status run_bwd(const BwdParams& p, void* dw, cudaStream_t s) {
     constexpr int ES = ElemBytes<XT>::value;
     constexpr int EPV = 16 / ES;
     constexpr int KMAX = 32 / EPV;         // 32 elements of a row per thread at most
-    const int64_t nvec = p.n / EPV;
     const int streams = p.dres ? 3 : 2;
     const bool wide = (p.n * ES) % 16 == 0 && aligned_to(p.dy, 16) && aligned_to(p.r, 16) && aligned_to(p.dres, 16) &&
                       aligned_to(p.dx, 16) && aligned_to(p.w, 16);
     if (p.m > 0 && p.m <= kSmallRows)             // with dw or without: the same dx
         return wide ? run_bwd_small<XT, WT, EPV>(p, dw, s) : run_bwd_small<XT, WT, 1>(p, dw, s);
-    const bool vec = wide && aligned_to(p.part, 16) &&
+    // rows that are no multiple of 16 bytes, and weights anywhere: the same vectors, shifted
+    const bool shift = !(wide && aligned_to(p.part, 16));
+    const int64_t nvec = shift ? (p.n + 2 * EPV - 2) / EPV : p.n / EPV;
+    const bool vec = aligned_to(p.dy, 16) && aligned_to(p.r, 16) && aligned_to(p.dres, 16) && aligned_to(p.dx, 16) &&
                      nvec <= static_cast<int64_t>(BwdShape<XT, KMAX>::kThreads) * KMAX &&
                      streams * KMAX * 16LL * round32((nvec + KMAX - 1) / KMAX) <= kSmemPerSm;
     int64_t parts = 0;
@@ -969,10 +1097,7 @@ fp8q_status run_bwd(const BwdParams& p, void* dw, cudaStream_t s) {
     if (p.m == 0) {
         st = FP8Q_OK;
     } else if (vec) {
-        if (nvec <= BwdShape<XT, 1>::kThreads) st = run_bwd_vec<XT, WT, 1>(p, &parts, s);
-        else if (nvec <= 2 * BwdShape<XT, 2>::kThreads) st = run_bwd_vec<XT, WT, 2>(p, &parts, s);
-        else if (KMAX == 4 || nvec <= 4 * BwdShape<XT, 4>::kThreads) st = run_bwd_vec<XT, WT, 4>(p, &parts, s);
-        else st = run_bwd_vec<XT, WT, KMAX>(p, &parts, s);
+        st = shift ? run_bwd_vec_k<XT, WT, true>(p, nvec, &parts, s) : run_bwd_vec_k<XT, WT, false>(p, nvec, &parts, s);
     } else {
         const int64_t cap = static_cast<int64_t>(sm_count()) * 8;
         if (p.n <= 4096) {

@@ -295,8 +295,8 @@ def test_forward_many_wide_rows(fp8q, m, n, group):
         check_forward(fp8q, x, r, w, group)
 
 
-# widths and pointers that no vector fits: single elements in registers up to 8192 columns forward
-# and 4096 backward, element by element from memory above
+# widths that no vector fits: single elements in registers up to 8192 columns forward, element by
+# element from memory above; backward aligned vectors that begin and end in other rows
 @pytest.mark.parametrize("dt", [BF16, F32])
 @pytest.mark.parametrize("res", [False, True])
 @pytest.mark.parametrize("m,n", [(700, 1001), (520, 100), (530, 4095), (513, 4097), (515, 8191), (3, 8193), (1, 1), (600, 2)])
@@ -314,3 +314,44 @@ def test_odd_widths(fp8q, dt, res, m, n):
     if res:
         assert torch.equal(out.t.view(m, n).double(), r64)
     check_backward(fp8q, m, n, dt, res)
+
+
+# rows that are no multiple of 16 bytes, each start inside a vector, with several rows a thread and
+# with one, up to the widest row and above it
+@pytest.mark.parametrize("dt,w32", [(BF16, False), (F16, True), (F32, False)])
+@pytest.mark.parametrize("res", [False, True])
+@pytest.mark.parametrize("m,n", [(1500, 2049), (1501, 2050), (1502, 2051), (1503, 2052), (1504, 2053), (1505, 2054), (1506, 2055),
+                                 (9999, 9), (20001, 65), (6001, 100), (2001, 3585), (1201, 7169), (700, 18001), (520, 20473),
+                                 (513, 20481), (600, 1), (601, 7)])
+def test_backward_shifted_rows(fp8q, dt, w32, res, m, n):
+    check_backward(fp8q, m, n, dt, res, w32=w32)
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_backward_shifted_rows_keep_apart(fp8q, dt, bad):
+    """What one row holds reaches no other row's gradient, though they share vectors."""
+    m, n = 1300, 1003
+    x, _, w = make(m, n, dt, False)
+    dy = torch.randn(m, n, device="cuda").to(dt)
+    _, rstd, _ = P.norm(x, w, None, EPS)
+    rstd = rstd.view(-1).float()
+    want, got = torch.empty_like(x), torch.empty_like(x)
+    fp8q.fp8q_rms_norm_bwd(dy, x, w, rstd, want)
+    dy[::2], x[::2] = bad, bad
+    fp8q.fp8q_rms_norm_bwd(dy, x, w, rstd, got)
+    assert torch.equal(got[1::2], want[1::2])
+    assert got[::2].isnan().all()
+
+
+def test_backward_shifted_rows_in_place(fp8q):
+    """A part of a larger buffer: the rows before and behind it are left as they were."""
+    m, n = 1201, 1001
+    x, _, w = make(m, n, BF16, False)
+    dy = torch.randn(m, n, device="cuda").to(BF16)
+    _, rstd, _ = P.norm(x, w, None, EPS)
+    rstd = rstd.view(-1).float()
+    want, buf = torch.empty_like(x), torch.full((m + 16, n), 7.0, device="cuda", dtype=BF16)
+    fp8q.fp8q_rms_norm_bwd(dy, x, w, rstd, want)
+    fp8q.fp8q_rms_norm_bwd(dy, x, w, rstd, buf[8:8 + m])
+    assert torch.equal(buf[8:8 + m], want) and (buf[:8] == 7).all() and (buf[8 + m:] == 7).all()
