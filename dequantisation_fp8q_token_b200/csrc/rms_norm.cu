@@ -79,7 +79,7 @@ __device__ __forceinline__ Weights<WT, N> load_weights(const uint8_t* __restrict
 }
 // the same from any place and alignment; zeros for elements outside the row's 0 .. n - 1
 template <int WT, int N>
-__device__ __forceinline__ Weights<WT, N> load_weights_any(const uint8_t* __restrict__ w, int e, int n) {
+__device__ __forceinline__ Weights<WT, N> load_weights_any(const uint8_t* w, int e, int n) {
     using Bits = std::conditional_t<ElemBytes<WT>::value == 4, uint32_t, uint16_t>;
     Weights<WT, N> r;
     uint32_t* out = reinterpret_cast<uint32_t*>(r.v);
@@ -90,7 +90,7 @@ __device__ __forceinline__ Weights<WT, N> load_weights_any(const uint8_t* __rest
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int c = e + j * PER + i;
-            if (c >= 0 && c < n) out[j] |= static_cast<uint32_t>(__ldg(reinterpret_cast<const Bits*>(w) + c)) << (16 * i);
+            if (c >= 0 && c < n) out[j] |= static_cast<uint32_t>(reinterpret_cast<const Bits*>(w)[c]) << (16 * i);
         }
     }
     return r;
@@ -284,12 +284,12 @@ rms_norm_vec_kernel(const FwdParams p) {
     }
 }
 
-// Forward to y for widths and pointers that no vector fits, up to 8192
+// Forward to y for tensors that are not at 16-byte addresses, up to 8192
 // columns: the vector kernel's plan with single elements (element k of thread
 // t is k * blockDim.x + t), so a row is still read once and a thread's loads
 // are in flight together.  Bound by the load and store instructions: bf16
 // 16384 x 1001 with a residual 45.8 us (the generic kernel 111.7), 4096 x 7169
-// 122 (159), 16384 x 100 without one 6.7 (29.4).
+// 122 (159), 16384 x 100 without one 6.7 (29.4), timed at 16-byte addresses.
 template <int XT, int WT, int K>
 __global__ void __launch_bounds__(512)
 rms_norm_elem_kernel(const FwdParams p) {
@@ -329,6 +329,91 @@ rms_norm_elem_kernel(const FwdParams p) {
         const int c = threadIdx.x + k * tpr;
         f[k] = __fmul_rn(__fmul_rn(f[k], rstd), elem_load<WT>(p.w + min(c, last) * WS));
         if (live && c <= last) elem_store<XT>(p.y + (base + c) * ES, f[k]);
+    }
+}
+
+// Forward to y for rows that are no multiple of 16 bytes (and weights
+// anywhere): the tensors' own aligned vectors, so a row starts `off` elements
+// inside its first one.  A vector that holds elements of another row as well
+// is read and written by elements, so no row touches another's.  The weights
+// come one by one from L1.  With a residual bf16 4096 x 7169 60.0 us (0.60 of
+// the copy bandwidth), 16384 x 1001 29.4, fp32 5060 x 5690 73.6 (0.95); single
+// elements throughout took 122, 45.9 and 121.
+template <int XT, int WT, int K>
+__global__ void __launch_bounds__(1024)
+rms_norm_shift_kernel(const FwdParams p) {
+    constexpr int ES = ElemBytes<XT>::value;
+    constexpr int EPV = 16 / ES;
+    __shared__ float sh[32 * 8];
+    pdl_begin();
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+    const bool live = row < p.m;
+    const int64_t base = row * p.n;
+    const int n = static_cast<int>(p.n), off = static_cast<int>(base & (EPV - 1));
+    const int at = static_cast<int>(threadIdx.x) * EPV - off, pitch = blockDim.x * EPV;    // columns
+    auto has = [&](int k) { return live && at + k * pitch < n; };
+    auto edge = [&](int k) { return at + k * pitch < 0 || at + k * pitch + EPV > n; };
+    auto load = [&](const uint8_t* t, int k) {
+        if (!edge(k)) return load_vec_plain<16>(t + (base + at + k * pitch) * ES);
+        const uint4 w = load_weights_any<XT, EPV>(t + base * ES, at + k * pitch, n).v[0];
+        Vec<16> v;
+        v.w[0] = w.x; v.w[1] = w.y; v.w[2] = w.z; v.w[3] = w.w;
+        return v;
+    };
+    auto store = [&](uint8_t* t, int k, const Vec<16>& v) {
+        uint8_t* dst = t + (base + at + k * pitch) * ES;
+        if (!edge(k)) {
+            store_vec<16>(dst, v);
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < EPV; ++j) {
+            const int c = at + k * pitch + j;
+            if (c < 0 || c >= n) continue;
+            if constexpr (ES == 4) *reinterpret_cast<uint32_t*>(dst + 4 * j) = v.w[j];
+            else *reinterpret_cast<uint16_t*>(dst + 2 * j) = static_cast<uint16_t>(v.w[j / 2] >> (16 * (j & 1)));
+        }
+    };
+    Vec<16> v[K], u[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        if (has(k)) {
+            v[k] = load(p.x, k);
+            if (p.res) u[k] = load(p.res, k);
+        }
+    }
+    float2 f[K][EPV / 2];
+    float2 sum = both(0.0f);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+#pragma unroll
+        for (int j = 0; j < EPV / 2; ++j) f[k][j] = both(0.0f);
+        if (has(k)) {
+            unpack<XT, 16>(v[k], f[k]);
+            if (p.res) {
+                float2 g[EPV / 2];
+                unpack<XT, 16>(u[k], g);
+#pragma unroll
+                for (int j = 0; j < EPV / 2; ++j) f[k][j] = __fadd2_rn(f[k][j], g[j]);
+                v[k] = pack<XT, 16>(f[k]);
+                store(p.res_out, k, v[k]);
+                if constexpr (XT != kF32) unpack<XT, 16>(v[k], f[k]);   // the stored sum is what is normed
+            }
+#pragma unroll
+            for (int j = 0; j < EPV / 2; ++j) sum = __ffma2_rn(f[k][j], f[k][j], sum);
+        }
+    }
+    const float rstd = rstd_of(row_sum(__fadd_rn(sum.x, sum.y), sh), p.inv_n, p.eps);
+    if (live && p.rstd && threadIdx.x == 0) p.rstd[row] = rstd;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        if (has(k)) {
+            float2 w[EPV / 2];
+            unpack_weights<WT, EPV>(load_weights_any<WT, EPV>(p.w, at + k * pitch, n), w);
+#pragma unroll
+            for (int j = 0; j < EPV / 2; ++j) f[k][j] = __fmul2_rn(__fmul2_rn(f[k][j], both(rstd)), w[j]);
+            store(p.y, k, pack<XT, 16>(f[k]));
+        }
     }
 }
 
@@ -981,6 +1066,16 @@ fp8q_status run_fwd(const FwdParams& p0, cudaStream_t s) {
             p.lanes_log2 = ilog2c(lanes);
         }
         if (ok) vb = b;
+    }
+    const int64_t nshift = (p.n + 2 * (16 / ES) - 2) / (16 / ES);
+    if (!vb && !p.q && nshift <= 1024 * 4 && aligned_to(p.x, 16) && aligned_to(p.res, 16) && aligned_to(p.res_out, 16) &&
+        aligned_to(p.y, 16)) {
+        const int k = nshift <= 256 ? 1 : nshift <= 2048 ? 2 : 4;
+        const int tpr = round32((nshift + k - 1) / k), rows = tpr >= 256 ? 1 : 256 / tpr < 8 ? 256 / tpr : 8;
+        const dim3 grid(static_cast<unsigned>((p.m + rows - 1) / rows)), block(tpr, rows);
+        return cuda_status(k == 1   ? launch_kernel(rms_norm_shift_kernel<XT, WT, 1>, grid, block, s, p)
+                           : k == 2 ? launch_kernel(rms_norm_shift_kernel<XT, WT, 2>, grid, block, s, p)
+                                    : launch_kernel(rms_norm_shift_kernel<XT, WT, 4>, grid, block, s, p));
     }
     if (!vb && !p.q && p.n <= 8192) {
         const int k = p.n <= 4096 ? 8 : 16;

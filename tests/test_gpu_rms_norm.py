@@ -295,8 +295,7 @@ def test_forward_many_wide_rows(fp8q, m, n, group):
         check_forward(fp8q, x, r, w, group)
 
 
-# widths that no vector fits: single elements in registers up to 8192 columns forward, element by
-# element from memory above; backward aligned vectors that begin and end in other rows
+# widths that no vector fits: aligned vectors that begin and end in other rows
 @pytest.mark.parametrize("dt", [BF16, F32])
 @pytest.mark.parametrize("res", [False, True])
 @pytest.mark.parametrize("m,n", [(700, 1001), (520, 100), (530, 4095), (513, 4097), (515, 8191), (3, 8193), (1, 1), (600, 2)])
@@ -355,3 +354,54 @@ def test_backward_shifted_rows_in_place(fp8q):
     fp8q.fp8q_rms_norm_bwd(dy, x, w, rstd, want)
     fp8q.fp8q_rms_norm_bwd(dy, x, w, rstd, buf[8:8 + m])
     assert torch.equal(buf[8:8 + m], want) and (buf[:8] == 7).all() and (buf[8 + m:] == 7).all()
+
+
+def check_plain_forward(fp8q, dt, res, m, n, w32=False, offset=0):
+    x, r, w = make(m, n, dt, res, w32, seed=11)
+    if offset:
+        x = shifted(x, offset)
+    y, rstd = Guarded(m * n, dt), Guarded(m, F32)
+    out = Guarded(m * n, dt) if res else None
+    fp8q.fp8q_rms_norm_quant(x, w, y=y.t, residual=r, residual_out=out.t.view(m, n) if res else None, rstd=rstd.t, eps=EPS)
+    for g in (y, rstd, out):
+        if g is not None:
+            g.check()
+    r64, rstd64, v = P.norm(x, w, r, EPS)
+    assert ((rstd.t.double() - rstd64.view(-1)).abs() <= rel(n) * rstd64.view(-1)).all()
+    assert ((y.t.view(m, n).double() - v).abs() <= v.abs() * (rel(n) + P.half_step(dt)) + P.tiny(dt)).all()
+    if res:
+        assert torch.equal(out.t.view(m, n).double(), r64)
+        # the sum in the place of x, and of the residual
+        for place in (0, 1):
+            a, b, y2 = x.clone(), r.clone(), torch.empty_like(x)
+            fp8q.fp8q_rms_norm_quant(a, w, y=y2, residual=b, residual_out=(a, b)[place], eps=EPS)
+            assert torch.equal((a, b)[place].view(-1), out.t)
+            # an aligned copy of an unaligned x is summed in another order, so its y is held to the
+            # bound that holds for every order and not to the bits
+            assert ((y2.double() - v).abs() <= v.abs() * (rel(n) + P.half_step(dt)) + P.tiny(dt)).all()
+            assert offset or torch.equal(y2.view(-1), y.t)
+
+
+@pytest.mark.parametrize("dt,w32", [(BF16, False), (F16, True), (F32, False)])
+@pytest.mark.parametrize("res", [False, True])
+@pytest.mark.parametrize("m,n", [(1, 1), (5, 3), (17, 9), (200, 2049), (201, 2050), (202, 2051), (203, 2052), (204, 2053), (205, 2054),
+                                 (206, 2055), (3001, 65), (5, 4097), (40, 8191), (31, 16385), (9, 18001), (3, 32753), (3, 32769)])
+def test_forward_shifted_rows(fp8q, dt, w32, res, m, n):
+    check_plain_forward(fp8q, dt, res, m, n, w32)
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("m,n", [(33, 1001), (7, 8191), (5, 8193)])
+def test_forward_shifted_addresses(fp8q, dt, m, n):
+    check_plain_forward(fp8q, dt, True, m, n, offset=1)
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_forward_shifted_rows_keep_apart(fp8q, dt):
+    x, r, w = make(300, 1003, dt, True)
+    want, got, out = torch.empty_like(x), torch.empty_like(x), torch.empty_like(x)
+    fp8q.fp8q_rms_norm_quant(x, w, y=want, residual=r, residual_out=out, eps=EPS)
+    x[::2] = float("nan")
+    fp8q.fp8q_rms_norm_quant(x, w, y=got, residual=r, residual_out=out, eps=EPS)
+    assert torch.equal(got[1::2], want[1::2])
+    assert got[::2].isnan().all()
