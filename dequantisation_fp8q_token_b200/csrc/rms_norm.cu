@@ -12,6 +12,7 @@
 // computed.  Every sum is fp32; y is rounded once, to T or to fp8.
 #include "fp8q_device.cuh"
 #include "fp8q_internal.h"
+#include "rms_norm_plan.h"
 
 #include <type_traits>
 
@@ -533,19 +534,11 @@ template <int BYTES> __device__ __forceinline__ void st_shared_zero(uint32_t a) 
     else asm volatile("st.shared.b16 [%0], %1;" :: "r"(a), "h"(static_cast<uint16_t>(0)) : "memory");
 }
 
-constexpr int kBwdMaxStages = 4;
-// Threads of a CTA at most, and registers a thread that its bounds leave: up to
-// 8 elements of a row a thread 512 and 64, up to 16 448 and 72 (two CTAs an
-// SM), for more 640 and 96.
-template <int XT, int K> struct BwdShape {
-    static constexpr int kElems = K * 16 / ElemBytes<XT>::value;
-    static constexpr int kThreads = kElems <= 8 ? 512 : kElems <= 16 ? 448 : 640;
-    static constexpr int kMinCtas = kElems <= 16 ? 2 : 1;
-    static constexpr int kRegs = kElems <= 8 ? 64 : kElems <= 16 ? 72 : 96;
-};
+// elements of a row that a thread holds
+template <int XT, int K> struct BwdElems { static constexpr int N = K * 16 / ElemBytes<XT>::value; };
 
 template <int XT, int WT, int K, bool SHIFT>
-__global__ void __launch_bounds__(BwdShape<XT, K>::kThreads, BwdShape<XT, K>::kMinCtas)
+__global__ void __launch_bounds__(bwd_threads(BwdElems<XT, K>::N), bwd_min_ctas(BwdElems<XT, K>::N))
 rms_norm_bwd_vec_kernel(const BwdParams p) {
     constexpr int ES = ElemBytes<XT>::value;
     constexpr int EPV = 16 / ES;
@@ -1122,43 +1115,34 @@ fp8q_status run_dw(const float* part, int64_t parts, int64_t n, void* dw, cudaSt
                                      n, out));
 }
 
-constexpr int kSmemPerSm = 222 * 1024;     // dynamic shared memory that CTAs of one SM may share here
-
 template <int XT, int WT, int K, bool SHIFT>
-fp8q_status run_bwd_vec(const BwdParams& p0, int64_t nvec, int64_t* parts, cudaStream_t s) {
+fp8q_status run_bwd_vec(const BwdParams& p0, const BwdPlan& plan, int64_t* parts, cudaStream_t s) {
     constexpr int EPV = 16 / ElemBytes<XT>::value;
     BwdParams p = p0;
-    const int tpr = round32((nvec + K - 1) / K);
-    using Shape = BwdShape<XT, K>;
-    const int rows = Shape::kThreads / tpr;
-    const int stage = (p.dres ? 3 : 2) * K * 16 * tpr * rows;
-    // two CTAs an SM where their registers and two stages each fit, else one
-    const int ctas = 2 * Shape::kRegs * tpr * rows <= 65536 && kSmemPerSm / 2 >= 2 * stage ? 2 : 1;
-    const int per_cta = kSmemPerSm / ctas;
-    p.stages = per_cta / stage < kBwdMaxStages ? per_cta / stage : kBwdMaxStages;
-    const int smem = p.stages * stage;
+    p.stages = plan.stages;
     auto kernel = rms_norm_bwd_vec_kernel<XT, WT, K, SHIFT>;
     static std::atomic<bool> allowed[64];
     const cudaError_t e = allow_smem(kernel, kSmemPerSm, allowed);
     if (e != cudaSuccess) return cuda_status(e);
-    const int64_t cap = static_cast<int64_t>(ctas) * sm_count(), want = (p.m + rows - 1) / rows;
+    const int64_t cap = static_cast<int64_t>(plan.ctas) * sm_count(), want = (p.m + plan.rows - 1) / plan.rows;
     *parts = want < cap ? want : cap;
     if (SHIFT && want > cap) {          // several turns: each moves a thread by a multiple of EPV elements
         int64_t turn = EPV;
-        while (turn > 1 && (turn / 2) * rows * p.n % EPV == 0) turn /= 2;
+        while (turn > 1 && (turn / 2) * plan.rows * p.n % EPV == 0) turn /= 2;
         if (cap < turn) return FP8Q_ERR_CUDA;      // not reached: every such GPU has more SMs
         *parts = cap - cap % turn;
     }
-    return cuda_status(launch_kernel_smem(kernel, dim3(static_cast<unsigned>(*parts)), dim3(tpr, rows), smem, s, p));
+    return cuda_status(launch_kernel_smem(kernel, dim3(static_cast<unsigned>(*parts)), dim3(plan.tpr, plan.rows), plan.smem,
+                                          s, p));
 }
 
 template <int XT, int WT, bool SHIFT>
-fp8q_status run_bwd_vec_k(const BwdParams& p, int64_t nvec, int64_t* parts, cudaStream_t s) {
-    constexpr int KMAX = 2 * ElemBytes<XT>::value;         // 32 elements of a row per thread at most
-    if (nvec <= BwdShape<XT, 1>::kThreads) return run_bwd_vec<XT, WT, 1, SHIFT>(p, nvec, parts, s);
-    if (nvec <= 2 * BwdShape<XT, 2>::kThreads) return run_bwd_vec<XT, WT, 2, SHIFT>(p, nvec, parts, s);
-    if (KMAX == 4 || nvec <= 4 * BwdShape<XT, 4>::kThreads) return run_bwd_vec<XT, WT, 4, SHIFT>(p, nvec, parts, s);
-    return run_bwd_vec<XT, WT, KMAX, SHIFT>(p, nvec, parts, s);
+fp8q_status run_bwd_vec_k(const BwdParams& p, const BwdPlan& plan, int64_t* parts, cudaStream_t s) {
+    if (plan.k == 1) return run_bwd_vec<XT, WT, 1, SHIFT>(p, plan, parts, s);
+    if (plan.k == 2) return run_bwd_vec<XT, WT, 2, SHIFT>(p, plan, parts, s);
+    if constexpr (XT == kF32)
+        if (plan.k == 8) return run_bwd_vec<XT, WT, 8, SHIFT>(p, plan, parts, s);
+    return run_bwd_vec<XT, WT, 4, SHIFT>(p, plan, parts, s);
 }
 
 template <int XT, int WT, int V>
@@ -1175,24 +1159,21 @@ template <int XT, int WT>
 fp8q_status run_bwd(const BwdParams& p, void* dw, cudaStream_t s) {
     constexpr int ES = ElemBytes<XT>::value;
     constexpr int EPV = 16 / ES;
-    constexpr int KMAX = 32 / EPV;         // 32 elements of a row per thread at most
-    const int streams = p.dres ? 3 : 2;
     const bool wide = (p.n * ES) % 16 == 0 && aligned_to(p.dy, 16) && aligned_to(p.r, 16) && aligned_to(p.dres, 16) &&
                       aligned_to(p.dx, 16) && aligned_to(p.w, 16);
     if (p.m > 0 && p.m <= kSmallRows)             // with dw or without: the same dx
         return wide ? run_bwd_small<XT, WT, EPV>(p, dw, s) : run_bwd_small<XT, WT, 1>(p, dw, s);
     // rows that are no multiple of 16 bytes, and weights anywhere: the same vectors, shifted
     const bool shift = !(wide && aligned_to(p.part, 16));
-    const int64_t nvec = shift ? (p.n + 2 * EPV - 2) / EPV : p.n / EPV;
-    const bool vec = aligned_to(p.dy, 16) && aligned_to(p.r, 16) && aligned_to(p.dres, 16) && aligned_to(p.dx, 16) &&
-                     nvec <= static_cast<int64_t>(BwdShape<XT, KMAX>::kThreads) * KMAX &&
-                     streams * KMAX * 16LL * round32((nvec + KMAX - 1) / KMAX) <= kSmemPerSm;
+    const BwdPlan plan = bwd_plan(ES, p.n, shift, p.dres ? 3 : 2);
+    const bool vec = plan.k != 0 && aligned_to(p.dy, 16) && aligned_to(p.r, 16) && aligned_to(p.dres, 16) &&
+                     aligned_to(p.dx, 16);
     int64_t parts = 0;
     fp8q_status st;
     if (p.m == 0) {
         st = FP8Q_OK;
     } else if (vec) {
-        st = shift ? run_bwd_vec_k<XT, WT, true>(p, nvec, &parts, s) : run_bwd_vec_k<XT, WT, false>(p, nvec, &parts, s);
+        st = shift ? run_bwd_vec_k<XT, WT, true>(p, plan, &parts, s) : run_bwd_vec_k<XT, WT, false>(p, plan, &parts, s);
     } else {
         const int64_t cap = static_cast<int64_t>(sm_count()) * 8;
         if (p.n <= 4096) {

@@ -405,3 +405,30 @@ def test_forward_shifted_rows_keep_apart(fp8q, dt):
     fp8q.fp8q_rms_norm_quant(x, w, y=got, residual=r, residual_out=out, eps=EPS)
     assert torch.equal(got[1::2], want[1::2])
     assert got[::2].isnan().all()
+
+
+# widths between those above: two rows a CTA and one, in fp32 the width from which memory for a row
+# in flight, and not threads, says how many
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("res", [False, True])
+@pytest.mark.parametrize("n", [8192, 9216, 9217, 9220, 10237, 10240, 10244, 12288, 16384])
+def test_backward_many_wide_rows(fp8q, dt, res, n):
+    check_backward(fp8q, 600, n, dt, res)
+
+
+def test_gradient_of_many_wide_fp32_rows(fp8q):
+    m, n = 700, 10240
+    x, r, w = make(m, n, F32, True)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    dy, dr = torch.randn(m, n, generator=g, device="cuda"), torch.randn(m, n, generator=g, device="cuda")
+    for t in (x, r, w):
+        t.requires_grad_(True)
+    gx, gr, gw = torch.autograd.grad(fp8q.rms_norm(x, w, residual=r, eps=EPS), (x, r, w), (dy, dr))
+    r64, rstd64, _ = P.norm(x.detach(), w.detach(), r.detach(), EPS)
+    want, want_w, mag, mag_w = P.norm_grad(r64, w.detach(), rstd64, dy, dr)
+    # the forward's rstd is within rel(n), beside the backward's own roundings; it enters dx up to three times
+    k = (max(32, n / 256) + 20) * P.U + 3 * rel(n)
+    assert ((gx.double() - want).abs() <= k * mag + want.abs() * P.half_step(F32) + P.tiny(F32)).all()
+    assert torch.equal(gx, gr)
+    tol = ((m + 64 + 4) * P.U + rel(n)) * mag_w + want_w.abs() * P.half_step(F32) + P.tiny(F32)
+    assert ((gw.double() - want_w).abs() <= tol).all()
