@@ -482,7 +482,7 @@ rms_norm_generic_kernel(const FwdParams p) {
 // flight while earlier rows are reduced, and no barrier guards the slots.
 // bf16 4096 x 7168 with a residual: 40.3 us for dx (89% of the measured copy
 // bandwidth), 44.0 with dw.
-// SHIFT, for rows that are no multiple of 16 bytes (and weights anywhere): the
+// SHIFT, for rows of 16 bytes and more that are no multiple of them (and weights anywhere): the
 // tensors' own aligned vectors, so a row starts `off` elements inside its first
 // one.  A thread's vectors lie at the same columns in each of its rows when the
 // rows between them are a multiple of 16 bytes together, which the grid sees
@@ -579,8 +579,7 @@ rms_norm_bwd_vec_kernel(const BwdParams p) {
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 if (SHIFT && in_row[k]) {
-                    // the last row's last vector may end past the tensor
-                    const int bytes = row == p.m - 1 && at + k * pitch + EPV > n ? (n - at - k * pitch) * ES : 16;
+                    const int bytes = copy_bytes(row, p.m, at + k * pitch, n, ES);
                     cp_async16(slot(stage, 0, k), p.dy + o + k * pitch * ES, bytes);
                     cp_async16(slot(stage, 1, k), p.r + o + k * pitch * ES, bytes);
                     if (streams == 3) cp_async16(slot(stage, 2, k), p.dres + o + k * pitch * ES, bytes);
@@ -1163,7 +1162,7 @@ fp8q_status run_bwd(const BwdParams& p, void* dw, cudaStream_t s) {
                       aligned_to(p.dx, 16) && aligned_to(p.w, 16);
     if (p.m > 0 && p.m <= kSmallRows)             // with dw or without: the same dx
         return wide ? run_bwd_small<XT, WT, EPV>(p, dw, s) : run_bwd_small<XT, WT, 1>(p, dw, s);
-    // rows that are no multiple of 16 bytes, and weights anywhere: the same vectors, shifted
+    // rows that are no multiple of 16 bytes but as long, and weights anywhere: the same vectors, shifted
     const bool shift = !(wide && aligned_to(p.part, 16));
     const BwdPlan plan = bwd_plan(ES, p.n, shift, p.dres ? 3 : 2);
     const bool vec = plan.k != 0 && aligned_to(p.dy, 16) && aligned_to(p.r, 16) && aligned_to(p.dres, 16) &&

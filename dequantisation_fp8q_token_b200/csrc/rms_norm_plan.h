@@ -1,9 +1,15 @@
 // rms_norm_plan.h -- how the norm's backward vector kernel (rms_norm.cu) is
-// launched: plain host arithmetic on sizes, apart from the kernel so that it
-// can be swept without a GPU.
+// launched and how far its copies reach: plain arithmetic on sizes, apart from
+// the kernel so that it can be swept without a GPU.
 #pragma once
 
 #include <stdint.h>
+
+#ifdef __CUDACC__
+#define FP8Q_HOST_DEVICE __host__ __device__ __forceinline__
+#else
+#define FP8Q_HOST_DEVICE inline
+#endif
 
 namespace fp8q {
 
@@ -30,6 +36,7 @@ struct BwdPlan {
 // row's; streams: tensors that are read (dy, r and perhaps dres).
 inline BwdPlan bwd_plan(int es, int64_t n, bool shift, int streams) {
     const int epv = 16 / es, kmax = 32 / epv;              // 32 elements of a row per thread at most
+    if (shift && n < epv) return {};       // a vector would hold more rows than two, and end past the tensor with any
     const int64_t nvec = shift ? (n + 2 * epv - 2) / epv : n / epv;
     for (int k = 1; k <= kmax; k *= 2) {
         const int threads = bwd_threads(k * epv);
@@ -51,6 +58,12 @@ inline BwdPlan bwd_plan(int es, int64_t n, bool shift, int streams) {
         return b;
     }
     return {};
+}
+
+// Bytes of the 16 at column `at` of a row that its tensor holds.  Rows are at
+// least a vector long (bwd_plan), so only the last one's last vector ends past it.
+FP8Q_HOST_DEVICE int copy_bytes(int64_t row, int64_t m, int at, int n, int es) {
+    return row == m - 1 && at + 16 / es > n ? (n - at) * es : 16;
 }
 
 }  // namespace fp8q

@@ -25,3 +25,7 @@ def run_program(name, tmp_path):
 
 def test_every_backward_launch_has_room_for_a_row(tmp_path):
     assert run_program("rms_norm_plan_check", tmp_path).startswith("ok: ")
+
+
+def test_no_copy_of_the_backward_pass_leaves_its_tensor(tmp_path):
+    assert run_program("rms_norm_copy_check", tmp_path).startswith("ok: ")
