@@ -178,10 +178,12 @@ __device__ __forceinline__ void store_cols_staged(typename OutT<YT>::T* base, in
     }
 }
 
-template <int N> __device__ __forceinline__ uint32_t absmax_of(const float (&v)[N]) {
+// the largest magnitude of the first `cols` values
+template <int N> __device__ __forceinline__ uint32_t absmax_below(const float (&v)[N], int cols) {
     uint32_t a = 0u;                                 // magnitude bits: a NaN stays the maximum
 #pragma unroll
-    for (int i = 0; i < N; ++i) a = max(a, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    for (int i = 0; i < N; ++i)
+        if (i < cols) a = max(a, __float_as_uint(v[i]) & 0x7FFFFFFFu);
     return a;
 }
 // the per-token cast's scales of a group
@@ -528,11 +530,21 @@ gated_mm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
             }
             if constexpr (OUT == kOutQuant) {
                 // the group's amax: this warp's half and, through shared memory, the other
-                // warp's.  Two buffers in turn: a warp is at most one tile ahead.
+                // warp's.  Two buffers in turn: a warp is at most one tile ahead.  Columns past I
+                // are zeros times the scales, which is a NaN where those are infinite: left out.
                 uint32_t mine = 0u;                      // magnitude bits: a NaN stays the maximum
+                const int cols = p.I - col0;             // of this warp's half that there are
+                if (cols >= kHalf) {
 #pragma unroll
-                for (int i = 0; i < kHalf / 2; ++i)
-                    mine = max(mine, max(__float_as_uint(accum[i].x) & 0x7FFFFFFFu, __float_as_uint(accum[i].y) & 0x7FFFFFFFu));
+                    for (int i = 0; i < kHalf / 2; ++i)
+                        mine = max(mine, max(__float_as_uint(accum[i].x) & 0x7FFFFFFFu, __float_as_uint(accum[i].y) & 0x7FFFFFFFu));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kHalf / 2; ++i) {
+                        if (2 * i < cols) mine = max(mine, __float_as_uint(accum[i].x) & 0x7FFFFFFFu);
+                        if (2 * i + 1 < cols) mine = max(mine, __float_as_uint(accum[i].y) & 0x7FFFFFFFu);
+                    }
+                }
                 s_amax[amax_phase][half][trow] = mine;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(amax0 + 8 * quarter);
@@ -685,7 +697,7 @@ gated_mm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
                     put(p.gu, row * 2 * p.I + p.I + col, p.align_gu, u);
                 }
             } else {
-                uint32_t amax = absmax_of(h);
+                uint32_t amax = absmax_below(h, p.I - col);
 #pragma unroll
                 for (int off = 16; off > 0; off >>= 1) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, off));
                 float scale, sinv;

@@ -474,3 +474,34 @@ def test_offsets_past_32_bits(fp8q):
     f = torch.cat((d * u64 * dv, d * v), 1)
     D = d8[rows].view(P.FP8[E5]).double() * sd.double()
     assert ((D - f).abs() <= f.abs() * (P.HALF[E5] + 1e-4) + 57344 * sd.item() * (P.TINY[E5] / 57344 + 1e-5)).all()
+
+
+# every form of the kernel that casts, with a last group shorter than 128 columns
+@pytest.mark.parametrize("how", ["scale of a row", "scale of a block", "code"])
+@pytest.mark.parametrize("M,I,K", [(3, 200, 256), (40, 200, 256), (100, 200, 1024), (300, 9504, 128), (300, 9001, 128),
+                                   (300, 9004, 128), (4, 9672, 256), (20, 9504, 256)])
+def test_an_infinite_row_has_infinite_scales_in_a_short_group_too(fp8q, M, I, K, how):
+    """Positive operands, so that an infinity among them makes its row's (or block's) gate, up and h
+    infinite and no value NaN; what stands past the last column is no part of its group."""
+    kb, ib, row = -(-K // 128), -(-I // 128), M // 2
+    fa = E5 if how == "code" else E4
+    a = torch.ones(M, K, device="cuda").to(P.FP8[fa])
+    w = torch.ones(I, K, device="cuda").to(P.FP8[E4])
+    sa, sg = torch.ones(M, kb, device="cuda"), torch.ones(ib, kb, device="cuda")
+    hit = torch.zeros(M, ib, dtype=torch.bool, device="cuda")
+    if how == "scale of a row":
+        sa[row, 0] = float("inf")
+        hit[row] = True
+    elif how == "scale of a block":
+        sg[ib - 1, 0] = float("inf")
+        hit[:, ib - 1] = True
+    else:
+        a.view(torch.uint8)[row, 7] = 0x7C
+        hit[row] = True
+    q, s = torch.empty(M, I, dtype=torch.uint8, device="cuda"), torch.empty(M, ib, device="cuda")
+    fp8q.fp8q_gated_mm_blockwise_quant(a, sa, w, sg, w, sg, q, s, fa=fa, fb=E4)
+    assert torch.equal(s.isinf(), hit) and (s > 0).all()
+    # h = K * sigmoid(K) * K = K^2 elsewhere (sigmoid(128) is 1), which is a group's amax: the largest code
+    cols = hit.repeat_interleave(128, 1)[:, :I]
+    assert (q[~cols] == 0x7E).all() and (q[cols] == 0x7F).all()
+    assert ((s[~hit].double() - K * K / 448).abs() <= 8 * P.U * K * K / 448).all()
