@@ -247,6 +247,11 @@ py::object rms_norm(const Tensor& x, const Tensor& weight, const MaybeTensor& re
 // ---------------------------------------------------------------------------
 // gated feed-forward block
 // ---------------------------------------------------------------------------
+// an unknown number is refused by the library, not cut to one that there is
+fp8q_activation activation(int64_t act) {
+    return static_cast<fp8q_activation>(act < 0 || act > INT_MAX ? -1 : act);
+}
+
 struct Operands {
     int64_t M, I, K;
     fp8q_format fa, fb;
@@ -292,7 +297,7 @@ void gated_mm_blockwise(const Tensor& a, const Tensor& scale_a, const Tensor& w_
     check(fp8q_gated_mm_blockwise(
               pa, o.fa, pointer_as<float>(scale_a, "scale_a", &a), pointer_as<uint8_t>(w_gate, "w_gate", &a),
               pointer_as<float>(scale_gate, "scale_gate", &a), pointer_as<uint8_t>(w_up, "w_up", &a),
-              pointer_as<float>(scale_up, "scale_up", &a), o.fb, o.M, o.I, o.K, static_cast<fp8q_activation>(act),
+              pointer_as<float>(scale_up, "scale_up", &a), o.fb, o.M, o.I, o.K, activation(act),
               dtype_code(out, "out"), pointer(out, "out", &a), status_word(status, a), stream_of(a, stream)),
           "fp8q_gated_mm_blockwise");
 }
@@ -309,7 +314,7 @@ void gated_mm_blockwise_quant(const Tensor& a, const Tensor& scale_a, const Tens
     check(fp8q_gated_mm_blockwise_quant(
               pa, o.fa, pointer_as<float>(scale_a, "scale_a", &a), pointer_as<uint8_t>(w_gate, "w_gate", &a),
               pointer_as<float>(scale_gate, "scale_gate", &a), pointer_as<uint8_t>(w_up, "w_up", &a),
-              pointer_as<float>(scale_up, "scale_up", &a), o.fb, o.M, o.I, o.K, static_cast<fp8q_activation>(act),
+              pointer_as<float>(scale_up, "scale_up", &a), o.fb, o.M, o.I, o.K, activation(act),
               static_cast<fp8q_format>(fmt), static_cast<fp8q_scale_rule>(rule), pointer_as<uint8_t>(q, "q", &a),
               pointer_as<float>(scale_inv, "scale_inv", &a), status_word(status, a), stream_of(a, stream)),
           "fp8q_gated_mm_blockwise_quant");
@@ -348,7 +353,8 @@ struct GatedLinear : torch::autograd::Function<GatedLinear> {
         return Parts<6>({T * K, 2 * I * K, 4, 4, static_cast<int64_t>(cast_workspace()), keep ? 2 * T * I * element : 0});
     }
 
-    static variable_list forward(AutogradContext* ctx, const Tensor& x_in, const Tensor& w_in, int64_t act, bool keep) {
+    static variable_list forward(AutogradContext* ctx, const Tensor& x_in, const Tensor& w_in, int64_t act_in, bool keep) {
+        const fp8q_activation act = activation(act_in);
         if ((x_in.scalar_type() != at::kBFloat16 && x_in.scalar_type() != at::kHalf) || x_in.scalar_type() != w_in.scalar_type())
             throw py::type_error("Only float16 and bfloat16 are allowed.");
         if (x_in.dim() < 1 || w_in.dim() != 2 || w_in.size(0) % 16 || x_in.size(-1) != w_in.size(1) || w_in.size(1) % 16)
@@ -370,7 +376,7 @@ struct GatedLinear : torch::autograd::Function<GatedLinear> {
                                         b + at_.at[4], cast_workspace(), FP8Q_SCALE_IEEE, st),
               "fp8q_cast_per_tensor_pair");
         check(fp8q_gated_mm(x8, FP8Q_E4M3FN, w8, w8 + I * K, FP8Q_E4M3FN, T, I, K, sx, sw, sw,
-                            static_cast<fp8q_activation>(act), dt, h.data_ptr(), keep ? b + at_.at[5] : nullptr, nullptr, st),
+                            act, dt, h.data_ptr(), keep ? b + at_.at[5] : nullptr, nullptr, st),
               "fp8q_gated_mm");
         if (keep) {
             ctx->save_for_backward({buf});

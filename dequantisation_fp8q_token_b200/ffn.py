@@ -134,10 +134,16 @@ def rms_norm_cast_to_fp8(x: torch.Tensor, weight: torch.Tensor, residual: Option
 # ---------------------------------------------------------------------------
 # gated feed-forward block
 # ---------------------------------------------------------------------------
+_ACTS = {"silu": ACT_SILU, "gelu_tanh": ACT_GELU_TANH}
+
+
 def _act_of(act) -> int:
     if isinstance(act, str):
-        return {"silu": ACT_SILU, "gelu_tanh": ACT_GELU_TANH}[act]
-    return int(act)
+        if act not in _ACTS:
+            raise ValueError(f'act must be "silu" or "gelu_tanh", got {act!r}')
+        return _ACTS[act]
+    code = int(act)
+    return code if 0 <= code <= 0x7FFFFFFF else -1           # an unknown number is refused by the library, uncut
 
 
 def fp8q_cast_per_tensor_pair(x0: torch.Tensor, q0: torch.Tensor, scale_inv0: torch.Tensor, x1: torch.Tensor,
@@ -184,6 +190,7 @@ def fp8q_gated_mm(a: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, sca
     """out[M, I] = act(gate) * up with gate = a @ w_gate.t() and up = a @ w_up.t() of fp8 codes a [M, K],
     w_gate and w_up [I, K] and per-tensor scales (fp32 [1] each).  gate_up: optional [M, 2 I] of out's
     dtype that receives gate and up for fp8q_gated_bwd_cast.  act: "silu" or "gelu_tanh"."""
+    act = _act_of(act)
     M, I, K, fa, fb = _gated_operands(a, w_gate, w_up, fa, fb)
     dev = a.device
     for t, name in ((scale_a, "scale_a"), (scale_gate, "scale_gate"), (scale_up, "scale_up")):
@@ -194,7 +201,7 @@ def fp8q_gated_mm(a: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, sca
     _check(lib().fp8q_gated_mm(
         _dev_ptr(a, "a"), fa, _dev_ptr(w_gate, "w_gate", dev), _dev_ptr(w_up, "w_up", dev), fb, M, I, K,
         _dev_ptr(scale_a, "scale_a", dev), _dev_ptr(scale_gate, "scale_gate", dev), _dev_ptr(scale_up, "scale_up", dev),
-        _act_of(act), _dtype_code(out, "out"), _dev_ptr(out, "out", dev), _dev_ptr(gate_up, "gate_up", dev),
+        act, _dtype_code(out, "out"), _dev_ptr(out, "out", dev), _dev_ptr(gate_up, "gate_up", dev),
         _dev_ptr(_status_word(status), "status", dev), _stream(stream, dev)), "fp8q_gated_mm")
 
 
@@ -222,6 +229,7 @@ def fp8q_gated_bwd_cast(dh: torch.Tensor, gate_up: torch.Tensor, q: torch.Tensor
                         workspace: torch.Tensor, act=ACT_SILU, fmt=E5M2, rule=SCALE_IEEE, stream=None) -> None:
     """The gradients of gate and up from dh [M, I] and fp8q_gated_mm's gate_up [M, 2 I], cast with one
     scale into codes q [M, 2 I] and scale_inv [1]; workspace as fp8q_cast_per_tensor's."""
+    act = _act_of(act)
     if dh.dim() != 2 or gate_up.dim() != 2 or gate_up.shape != (dh.shape[0], 2 * dh.shape[1]):
         raise ValueError(f"dh must be [M, I] and gate_up [M, 2 I], got {tuple(dh.shape)} and {tuple(gate_up.shape)}")
     if gate_up.dtype != dh.dtype:
@@ -231,7 +239,7 @@ def fp8q_gated_bwd_cast(dh: torch.Tensor, gate_up: torch.Tensor, q: torch.Tensor
     _need(q, 2 * M * I, "q", byte=True)
     _need(scale_inv, 1, "scale_inv", dtype=torch.float32)
     _check(lib().fp8q_gated_bwd_cast(
-        _dev_ptr(dh, "dh"), _dev_ptr(gate_up, "gate_up", dev), _dtype_code(dh, "dh"), M, I, _act_of(act), _fmt_of(fmt),
+        _dev_ptr(dh, "dh"), _dev_ptr(gate_up, "gate_up", dev), _dtype_code(dh, "dh"), M, I, act, _fmt_of(fmt),
         _dev_ptr(q, "q", dev), _dev_ptr(scale_inv, "scale_inv", dev), _dev_ptr(workspace, "workspace", dev),
         workspace.numel() * workspace.element_size(), _rule_of(rule), _stream(stream, dev)), "fp8q_gated_bwd_cast")
 
@@ -247,6 +255,7 @@ def gated_linear_fp8_blockwise(input: torch.Tensor, w_gate: torch.Tensor, scale_
                                w_up: torch.Tensor, scale_up: torch.Tensor, act="silu") -> torch.Tensor:
     """act(input @ w_gate.t()) * (input @ w_up.t()) on fp8 weights [I, K] with 128 x 128 block scales: the
     input is quantised per token, as linear_fp8_blockwise does; the output has the input's dtype."""
+    act = _act_of(act)
     x = input.contiguous().reshape(-1, input.shape[-1])
     q, s = per_token_cast_to_fp8(x)
     h = torch.empty((x.shape[0], w_gate.shape[0]), dtype=input.dtype, device=input.device)
@@ -268,6 +277,7 @@ def ffn_fp8_blockwise(input: torch.Tensor, w_gate: torch.Tensor, scale_gate: tor
     input to the output: (with norm_weight) the residual's addition, the norm and its cast; the gated
     products and the cast of their result; the down projection w_down [N, I].  Returns the output in
     the input's dtype, or (output, input + residual) when a residual is given."""
+    act = _act_of(act)
     x = input.contiguous().reshape(-1, input.shape[-1])
     r = None
     if norm_weight is None:

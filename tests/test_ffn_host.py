@@ -182,3 +182,33 @@ def test_the_plain_derivative_is_that_of_differences(act):
     assert (d - s * (1 + g * (1 - s) * dp)).abs().max() < 1e-12
     h = 1e-5
     assert (d - (plain64.act(g + h, act)[0] - plain64.act(g - h, act)[0]) / (2 * h)).abs().max() < 1e-9
+
+
+@pytest.mark.parametrize("act", ["gelu", "SiLU", ""])
+def test_an_unknown_activation_is_refused(L, act):
+    """By its name, before anything else is looked at."""
+    import dequantisation_fp8q_token_b200 as f
+    e4 = torch.float8_e4m3fn
+    a, w = torch.zeros(4, 256, dtype=e4), torch.zeros(64, 256, dtype=e4)
+    sa, sw, one = torch.ones(4, 2), torch.ones(1, 2), torch.ones(1)
+    h, gu = torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(4, 128, dtype=torch.bfloat16)
+    q, s, ws = torch.zeros(4, 64, dtype=e4), torch.zeros(4, 1), torch.zeros(8192, dtype=torch.uint8)
+    x, wx = torch.zeros(4, 256, dtype=torch.bfloat16), torch.zeros(64, 256, dtype=torch.bfloat16)
+    for call in (lambda: f.fp8q_gated_mm(a, w, w, one, one, one, h, act=act),
+                 lambda: f.fp8q_gated_mm_blockwise(a, sa, w, sw, w, sw, h, act=act),
+                 lambda: f.fp8q_gated_mm_blockwise_quant(a, sa, w, sw, w, sw, q, s, act=act),
+                 lambda: f.fp8q_gated_bwd_cast(h, gu, torch.zeros(4, 128, dtype=torch.uint8), one, ws, act=act),
+                 lambda: f.gated_linear_fp8(x, wx, act), lambda: f.gated_linear_fp8_blockwise(x, w, sw, w, sw, act),
+                 lambda: f.ffn_fp8(x, wx, torch.zeros(256, 32, dtype=torch.bfloat16), act),
+                 lambda: f.ffn_fp8_blockwise(x, w, sw, w, sw, torch.zeros(256, 64, dtype=e4), torch.ones(2, 1), act=act)):
+        with pytest.raises(ValueError, match="act must be"):
+            call()
+
+
+@pytest.mark.parametrize("act", [2, -1, 1 << 31, 1 << 32, (1 << 32) + 1, 1 << 70])
+def test_an_unknown_number_stays_unknown(L, act):
+    """What the binding hands on for it is refused by the library; nothing is cut to a number that there is."""
+    import dequantisation_fp8q_token_b200 as f
+    code = f.ffn._act_of(act)
+    assert L.fp8q_gated_bwd_cast(P, P, 2, 4, 32, code, 1, P, P, A, 8192, 0, None) == 4
+    assert [f.ffn._act_of(a) for a in ("silu", "gelu_tanh", f.ACT_SILU, f.ACT_GELU_TANH)] == [0, 1, 0, 1]

@@ -289,3 +289,14 @@ def test_blocks_of_few_tokens(fp8q, M):
     assert out.shape == r.shape == (M, 256) and out.isfinite().all() and torch.equal(r, x + x)
     assert fp8q.ffn_fp8_blockwise(x, wg, sg, wu, su, wd, sd).shape == (M, 256)
     assert fp8q.gated_linear_fp8_blockwise(x.view(M, 1, 256), wg, sg, wu, su).shape == (M, 1, 128)
+
+
+def test_activation_numbers_past_32_bits(fp8q):
+    ops, h, hs = fine(4, 64, 256), torch.zeros(4, 64, dtype=torch.uint8, device="cuda"), torch.zeros(4, 1, device="cuda")
+    x, w = rand(4, 256), rand(64, 256)
+    for act in (1 << 32, (1 << 32) + 1, -1):
+        for call in (lambda: fp8q.fp8q_gated_mm_blockwise_quant(*ops, h, hs, act=act), lambda: fp8q.gated_linear_fp8(x, w, act),
+                     lambda: fp8q.ffn._native().gated_linear_fp8(x, w, act)):
+            with pytest.raises(fp8q.Fp8qError) as e:
+                call()
+            assert e.value.status == 4
