@@ -58,9 +58,18 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in sources() + _deps() + [__file__])
 
 
+def torch_ext_tag() -> str:
+    """What _fp8q_torch.so is built for; the module holds it as `built_for`."""
+    import torch
+    return f"fp8q for torch {torch.__version__}, cxx11 abi {int(torch.compiled_with_cxx11_abi())}, {sys.implementation.cache_tag}"
+
+
 def torch_ext_up_to_date() -> bool:
     if not os.path.exists(TORCH_EXT):
         return False
+    with open(TORCH_EXT, "rb") as f:
+        if torch_ext_tag().encode() + b"\0" not in f.read():
+            return False
     t = os.path.getmtime(TORCH_EXT)
     return all(os.path.getmtime(p) <= t for p in (TORCH_SRC, os.path.join(INCLUDE, "fp8q.h"), __file__))
 
@@ -77,7 +86,8 @@ def build_torch_ext(force: bool = False, verbose: bool = False) -> str:
     tmp = TORCH_EXT + ".tmp.%d" % os.getpid()
     cuda_include = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
     cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-DTORCH_EXTENSION_NAME=_fp8q_torch",
-           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch.compiled_with_cxx11_abi(), "-I", INCLUDE]
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch.compiled_with_cxx11_abi(), f'-DFP8Q_BUILT_FOR="{torch_ext_tag()}"',
+           "-I", INCLUDE]
     for d in [*cpp_extension.include_paths(), cuda_include, sysconfig.get_paths()["include"]]:
         cmd += ["-isystem", d]
     cmd += [TORCH_SRC, "-o", tmp]

@@ -436,6 +436,7 @@ Tensor gated_linear_fp8(const Tensor& x, const Tensor& w, int64_t act) {
 
 PYBIND11_MODULE(TORCH_EXTENSION_NAME, m) {
     m.doc() = "The norm and feed-forward calls of libfp8q: marshalling and autograd";
+    m.attr("built_for") = FP8Q_BUILT_FOR;          // the build looks for it in the file
     py::register_local_exception_translator([](std::exception_ptr p) {
         try {
             if (p) std::rethrow_exception(p);
