@@ -4,8 +4,6 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include <atomic>
-
 #include "fp8q.h"
 
 #ifndef FP8Q_PDL
@@ -21,16 +19,11 @@ constexpr size_t kPerTensorWorkspaceBytes = kMaxPartials * sizeof(uint32_t);
 // number of SMs of the current device (cached per device)
 int sm_count();
 
-// Allow `kernel` `bytes` of dynamic shared memory, asked of the runtime once per device (`done`: a
-// static array of the caller's, one per kernel).
+// Allow `kernel` `bytes` of dynamic shared memory.  Asked at every call (0.12 us):
+// the limit belongs to the device's context, which a caller may make anew.
 template <typename Kernel>
-cudaError_t allow_smem(Kernel kernel, int bytes, std::atomic<bool> (&done)[64]) {
-    int dev = -1;
-    const bool known = cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64;
-    if (known && done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess && known) done[dev].store(true, std::memory_order_relaxed);
-    return e;
+cudaError_t allow_smem(Kernel kernel, int bytes) {
+    return cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
 // CTAs of `kernel` with `threads` threads that fit on one SM at once (>= 1)

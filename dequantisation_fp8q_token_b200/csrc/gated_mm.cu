@@ -34,6 +34,7 @@
 //   gated_pair_kernel             per-tensor scales, many tiles: 256 rows on
 //     CTA pairs (tcgen05.mma.cta_group::2), the even CTA loading the tile's
 //     rows of Wg and the odd one its rows of Wu.
+#include <atomic>
 #include <cstring>
 #include <type_traits>
 
@@ -962,8 +963,7 @@ template <bool FINE, int OUT, int MODE>
 cudaError_t launch_gated_mode(const CUtensorMap& ma, const CUtensorMap& mg, const CUtensorMap& mu, GatedParams& p,
                               uint32_t idesc, cudaStream_t s) {
     auto kernel = gated_mm_kernel<FINE, OUT, MODE>;
-    static std::atomic<bool> allowed[64];
-    const cudaError_t e = allow_smem(kernel, kGatedSmemBytes, allowed);
+    const cudaError_t e = allow_smem(kernel, kGatedSmemBytes);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kThreads);
@@ -1002,8 +1002,7 @@ Few few_rows(int64_t M, int64_t tiles_n) {
 int split_fit(int size) {
     static std::atomic<int> fit[kMaxSplit + 1][64];
     auto kernel = gated_mm_kernel<true, kOutQuant, kCluster>;
-    static std::atomic<bool> allowed[64];
-    if (allow_smem(kernel, kGatedSmemBytes, allowed) != cudaSuccess) return 1;
+    if (allow_smem(kernel, kGatedSmemBytes) != cudaSuccess) return 1;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kGatedSmemBytes;
@@ -1062,8 +1061,7 @@ template <int YT>
 cudaError_t launch_gated_pair(const CUtensorMap& ma, const CUtensorMap& mg, const CUtensorMap& mu, const GatedParams& p,
                               uint32_t idesc, cudaStream_t s) {
     auto kernel = pair::gated_pair_kernel<YT>;
-    static std::atomic<bool> allowed[64];
-    const cudaError_t e = allow_smem(kernel, pair::kGatedSmem, allowed);
+    const cudaError_t e = allow_smem(kernel, pair::kGatedSmem);
     if (e != cudaSuccess) return e;
     static std::atomic<int> fit[64];
     cudaLaunchConfig_t cfg = {};

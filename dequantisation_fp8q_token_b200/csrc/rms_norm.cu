@@ -1120,8 +1120,7 @@ fp8q_status run_bwd_vec(const BwdParams& p0, const BwdPlan& plan, int64_t* parts
     BwdParams p = p0;
     p.stages = plan.stages;
     auto kernel = rms_norm_bwd_vec_kernel<XT, WT, K, SHIFT>;
-    static std::atomic<bool> allowed[64];
-    const cudaError_t e = allow_smem(kernel, kSmemPerSm, allowed);
+    const cudaError_t e = allow_smem(kernel, kSmemPerSm);
     if (e != cudaSuccess) return cuda_status(e);
     const int64_t cap = static_cast<int64_t>(plan.ctas) * sm_count(), want = (p.m + plan.rows - 1) / plan.rows;
     *parts = want < cap ? want : cap;
