@@ -2,10 +2,9 @@
 // product's operands need.  The arithmetic is quant_scaled.cu's, bit for bit:
 // an amax pass that leaves one maximum per CTA, then a cast pass; here each
 // pass is one launch, whose first CTAs take one tensor and the others the
-// other.  For tensors that fit in L2 together, where the launches are what a
-// cast costs (bf16 300 x 1024 and 768 x 1024: 5.3 us, two casts 9.3; 300 x 4096 and
-// 2048 x 4096, 19 MB: 13.5 either way); larger
-// ones are cast one after the other, each with the L2 to itself.
+// other.  For whole aligned vectors of 16 MB together at most, where the launches
+// are what a cast costs (bf16 300 x 1024 and 768 x 1024: 5.3 us, two casts 9.3; 300 x
+// 4096 and 2048 x 4096, 19 MB: 13.5 either way); others are cast one after the other.
 #include "per_tensor_device.cuh"
 #include "fp8q_internal.h"
 

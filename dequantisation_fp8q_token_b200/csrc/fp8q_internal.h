@@ -69,7 +69,7 @@ fp8q_status launch_per_channel(const void* x, int xt, int64_t rows, int64_t cols
                                uint8_t* q, float* sinv, int rule, cudaStream_t s);
 fp8q_status launch_per_tensor(const void* x, int xt, int64_t numel, int fmt, uint8_t* q,
                               float* sinv, uint32_t* partials, int rule, cudaStream_t s);
-// two tensors of one type, in two launches where both fit in L2
+// two tensors of one type, in two launches where they are small and aligned (cast_pair.cu)
 fp8q_status launch_per_tensor_pair(const void* const (&x)[2], const int64_t (&numel)[2], uint8_t* const (&q)[2],
                                    float* const (&sinv)[2], int xt, int fmt, uint32_t* partials, int rule,
                                    cudaStream_t s);

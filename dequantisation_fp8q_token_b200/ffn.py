@@ -150,7 +150,8 @@ def fp8q_cast_per_tensor_pair(x0: torch.Tensor, q0: torch.Tensor, scale_inv0: to
                               q1: torch.Tensor, scale_inv1: torch.Tensor, workspace: torch.Tensor, fmt=E4M3FN,
                               rule=SCALE_IEEE, stream=None) -> None:
     """fp8q_cast_per_tensor_ex of two tensors of one dtype (a product's operands), with the same bytes, in two
-    launches where both fit in L2 together; workspace as fp8q_cast_per_tensor's."""
+    launches where they are 16 MB together at most, start on 16 bytes and are whole 16-byte vectors;
+    workspace as fp8q_cast_per_tensor's."""
     if x0.dtype != x1.dtype:
         raise TypeError("the two tensors must have one dtype")
     dev = x0.device

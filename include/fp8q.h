@@ -199,9 +199,11 @@ fp8q_status fp8q_cast_per_tensor_ex(const void* x, fp8q_dtype xt, int64_t numel,
 
 /*
  * The per-tensor casts of two tensors of one type, as a product's operands
- * need them: fp8q_cast_per_tensor_ex of each, with the same bytes, in two
- * kernels where both tensors fit in L2 together.  workspace and errors as
- * fp8q_cast_per_tensor_ex; nothing is written when either is refused.
+ * need them: fp8q_cast_per_tensor_ex of each, with the same bytes.  Two kernels
+ * do both where x0 and x1 are 16 MB together at most, each starts on 16 bytes
+ * and is a multiple of 16 bytes, and q0 and q1 start on a multiple of the codes
+ * of 16 bytes; other tensors are cast one after the other.  workspace and errors
+ * as fp8q_cast_per_tensor_ex; nothing is written when either is refused.
  */
 fp8q_status fp8q_cast_per_tensor_pair(const void* x0, int64_t numel0, uint8_t* q0, float* scale_inv0,
                                       const void* x1, int64_t numel1, uint8_t* q1, float* scale_inv1,
