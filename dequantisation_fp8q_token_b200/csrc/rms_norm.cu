@@ -288,9 +288,10 @@ rms_norm_vec_kernel(const FwdParams p) {
 // Forward to y for tensors that are not at 16-byte addresses, up to 8192
 // columns: the vector kernel's plan with single elements (element k of thread
 // t is k * blockDim.x + t), so a row is still read once and a thread's loads
-// are in flight together.  Bound by the load and store instructions: bf16
-// 16384 x 1001 with a residual 45.8 us (the generic kernel 111.7), 4096 x 7169
-// 122 (159), 16384 x 100 without one 6.7 (29.4), timed at 16-byte addresses.
+// are in flight together.  Bound by the load and store instructions.  One
+// element past a 16-byte address, the generic kernel's time after it: bf16 with
+// a residual 16384 x 1001 45.5 us (112), 4096 x 2048 24.6 (50.3), 4096 x 7168
+// 124 (159); 16384 x 100 without one 6.5 (29.0); fp32 600 x 2048 6.9 (10.3).
 template <int XT, int WT, int K>
 __global__ void __launch_bounds__(512)
 rms_norm_elem_kernel(const FwdParams p) {
@@ -804,9 +805,10 @@ rms_norm_dw_generic_kernel(const float* part, int parts, int64_t n, uint8_t* __r
 }
 
 // Backward, dx, for tensors that are not at 16-byte addresses, up to 4096
-// columns: as the forward's, one element at a time, dy and r read once (bf16
-// 16384 x 1001 48.3 us, the generic kernel 67.1; with 16 elements a thread
-// 4096 x 7169 took 107.7 and takes 103.8 there).
+// columns, and for rows narrower than a vector: as the forward's, one element at
+// a time, dy and r read once.  One element past a 16-byte address, bf16 with a
+// residual, the kernel below after it: 16384 x 1001 48.4 us (67.2), 4096 x 2048
+// 24.6 (31.1); at the widest, 4096 x 4096, it loses: 75.0 (60.7).
 template <int XT, int WT, int K>
 __global__ void __launch_bounds__(512)
 rms_norm_bwd_elem_kernel(const BwdParams p) {
@@ -874,9 +876,10 @@ rms_norm_bwd_dx_kernel(const BwdParams p) {
     }
 }
 // ... and COLS columns x one slice of the rows per CTA, 256 / COLS rows at a
-// time, for the partial sums of dw: 256 columns, or 32 where that leaves most
-// of the threads without one (bf16 16384 x 100: 13.9 us with dx, 22.2 with 256;
-// 4096 x 7169: 176 and 148)
+// time, for the partial sums of dw: 256 columns, or 32 up to 512, where 256 leave
+// many threads without one.  With dx, one element past a 16-byte address, 32 and
+// 256 columns: bf16 16384 x 100 13.9 and 20.7 us, 16384 x 500 31.4 and 33.3, with
+// a residual 4096 x 1000 26.0 and 20.9, 4096 x 7168 179 and 143.
 template <int XT, int COLS>
 __global__ void __launch_bounds__(256)
 rms_norm_bwd_part_kernel(const BwdParams p, int64_t rows_per_part) {
@@ -906,8 +909,11 @@ rms_norm_bwd_part_kernel(const BwdParams p, int64_t rows_per_part) {
 // CTAs take rows (dx) and the others columns (dw: 8 threads of V elements, 32
 // rows at a time), each reading dy and r for itself, which are in L2 by then.
 // No workspace.  Latency bound: bf16 300 x 7168 6.8 us against 9.6 in
-// two launches through partial sums, 512 x 18432 19.0 against 26.4.  V: elements of a 16-byte vector, or 1
-// for layouts that have none.
+// two launches through partial sums, 512 x 18432 19.0 against 26.4.  V: elements
+// of a 16-byte vector, or 1 for layouts that have none (with a residual, two
+// launches after it: bf16 1 x 1001 2.9 us (5.2), 200 x 1001 3.7 (6.2), fp32 512 x
+// 999 5.9 (7.8), bf16 512 x 7169 20.0 (20.1), 512 x 4097 14.7 (12.5), and 512 x 1024
+// at an odd address 5.9 (7.6)).
 // ---------------------------------------------------------------------------
 constexpr int kSmallRows = 512;
 
